@@ -7,7 +7,10 @@ package is the Python face of that ABI:
 * :mod:`csr_spmm_gb300._lib` -- the C entry points under their C names
   (``spmm_create``, ``spmm_csr_f32``, ...), pointers as integers;
 * :class:`Handle` and :func:`spmm` -- the same call taking torch CUDA tensors
-  (PyTorch supplies device memory and the current stream only).
+  (PyTorch supplies device memory and the current stream only);
+* :mod:`csr_spmm_gb300.lm` -- the operators at the two ends of a language
+  model, on torch CUDA tensors: :func:`embedding`, :func:`layer_norm`,
+  :func:`token_logprob` and their gradients.
 
 There is no CPU path: without the built library every call raises.
 """
@@ -25,7 +28,12 @@ from ._lib import (EXPORTED, SPMM_ERR_ALLOC, SPMM_ERR_CUDA, SPMM_ERR_DIMENSION_M
                    spmm_plan_order_rows_auto,
                    spmm_csr_squared_f32, spmm_csr_squared_f64, spmm_fw_argmin,
                    spmm_ilu0, ILU0_SINGULAR, ILU0_WAIT_TIMEOUT,
-                   spmm_reserve, spmm_set_profiling, status_string)
+                   spmm_reserve, spmm_set_profiling, status_string,
+                   SPMM_F32, SPMM_F16, SPMM_BF16, SPMM_TOP_MAX, spmm_reserve_lm, spmm_embedding,
+                   spmm_embedding_grad, spmm_layer_norm, spmm_layer_norm_grad, spmm_token_logprob,
+                   spmm_token_logprob_grad)
+from .lm import (embedding, embedding_grad, layer_norm, layer_norm_grad, token_logprob,
+                 token_logprob_grad)
 
 __all__ = ["Handle", "spmm", "csr_check", "SpmmError", "library", "spmm_create", "spmm_destroy",
            "spmm_reserve", "spmm_csr_f32", "spmm_csr_f64", "spmm_csr_check", "status_string",
@@ -35,7 +43,11 @@ __all__ = ["Handle", "spmm", "csr_check", "SpmmError", "library", "spmm_create",
            "spmm_fw_argmin", "fw_argmin", "spmm_ilu0", "ilu0", "Ilu0Error",
            "spmm_plan_csr_f64", "spmm_plan_order_rows", "spmm_row_order_bfs",
            "spmm_plan_csr_squared_f32", "spmm_plan_csr_squared_f64", "Plan",
-           "spmm_measure_fp64_fma_rate", "spmm_plan_order_rows_auto", "EXPORTED"]
+           "spmm_measure_fp64_fma_rate", "spmm_plan_order_rows_auto", "SPMM_F32", "SPMM_F16",
+           "SPMM_BF16", "SPMM_TOP_MAX", "spmm_reserve_lm", "spmm_embedding",
+           "spmm_embedding_grad", "spmm_layer_norm", "spmm_layer_norm_grad",
+           "spmm_token_logprob", "spmm_token_logprob_grad", "embedding", "embedding_grad",
+           "layer_norm", "layer_norm_grad", "token_logprob", "token_logprob_grad", "EXPORTED"]
 
 
 class Handle:
@@ -48,6 +60,10 @@ class Handle:
 
     def reserve(self, m: int, n: int, elem_size: int) -> None:
         spmm_reserve(self.ptr, m, n, elem_size)
+
+    def reserve_lm(self, rows: int, dim: int) -> None:
+        """Scratch of embedding_grad and layer_norm_grad for up to rows x dim inputs."""
+        spmm_reserve_lm(self.ptr, rows, dim)
 
     def close(self) -> None:
         if self.ptr:

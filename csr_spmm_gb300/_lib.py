@@ -32,7 +32,13 @@ EXPORTED = ("spmm_create", "spmm_destroy", "spmm_reserve", "spmm_csr_f32", "spmm
             "spmm_plan_create", "spmm_plan_destroy", "spmm_plan_csr_f32", "spmm_plan_csr_f64",
             "spmm_plan_order_rows", "spmm_row_order_bfs", "spmm_plan_csr_squared_f32",
             "spmm_plan_csr_squared_f64", "spmm_measure_fp64_fma_rate", "spmm_plan_order_rows_auto",
+            "spmm_reserve_lm", "spmm_embedding", "spmm_embedding_grad", "spmm_layer_norm",
+            "spmm_layer_norm_grad", "spmm_token_logprob", "spmm_token_logprob_grad",
             "spmm_status_string")
+
+# spmm_type_t
+SPMM_F32, SPMM_F16, SPMM_BF16 = 0, 1, 2
+SPMM_TOP_MAX = 32
 
 
 class SpmmProfile(ctypes.Structure):
@@ -139,6 +145,26 @@ def load_library(path: str) -> ctypes.CDLL:
     lib.spmm_plan_order_rows.restype = st
     lib.spmm_row_order_bfs.argtypes = [vp, vp, i64, vp]
     lib.spmm_row_order_bfs.restype = st
+    ty, f32 = ctypes.c_int, ctypes.c_float
+    lib.spmm_reserve_lm.argtypes = [vp, i64, i64]
+    lib.spmm_reserve_lm.restype = st
+    lib.spmm_embedding.argtypes = [vp, ty, f32, vp, i64, vp, i64, i64, i64, vp, i64, vp]
+    lib.spmm_embedding.restype = st
+    lib.spmm_embedding_grad.argtypes = [vp, ty, ty, f32, vp, i64, vp, i64, f32, vp, i64, i64, i64,
+                                        vp]
+    lib.spmm_embedding_grad.restype = st
+    lib.spmm_layer_norm.argtypes = [vp, ty, ty, vp, i64, i64, i64, vp, vp, f32, vp, i64, vp, vp,
+                                    vp]
+    lib.spmm_layer_norm.restype = st
+    lib.spmm_layer_norm_grad.argtypes = [vp, ty, ty, vp, i64, vp, i64, vp, vp, vp, i64, i64, vp,
+                                         i64, vp, vp, vp]
+    lib.spmm_layer_norm_grad.restype = st
+    lib.spmm_token_logprob.argtypes = [vp, ty, f32, vp, i64, i64, i64, vp, i32, vp, vp, vp, vp,
+                                       vp, vp]
+    lib.spmm_token_logprob.restype = st
+    lib.spmm_token_logprob_grad.argtypes = [vp, ty, f32, vp, i64, i64, i64, vp, vp, vp, vp, vp,
+                                            vp, i64, vp]
+    lib.spmm_token_logprob_grad.restype = st
     lib.spmm_status_string.argtypes = [ctypes.c_int]
     lib.spmm_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -348,4 +374,72 @@ def spmm_ilu0(handle, n, nnz, row_ptr, col_idx, values, depth, status, f64=False
     s = fn(handle, n, nnz, row_ptr, col_idx, values, depth, status, stream or None)
     if check:
         _check(s, "spmm_ilu0_f64" if f64 else "spmm_ilu0_f32")
+    return s
+
+
+def spmm_reserve_lm(handle, rows, dim) -> None:
+    """Scratch of the language-model gradients for up to `rows` rows of `dim` columns."""
+    _check(library().spmm_reserve_lm(handle, rows, dim), "spmm_reserve_lm")
+
+
+def spmm_embedding(handle, type_, scale, ids, tokens, table, ld_table, vocab, dim, out, ld_out,
+                   stream=0, check=True) -> int:
+    """out[t, :] = scale * table[ids[t], :] (device pointers, spmm_type_t)."""
+    s = library().spmm_embedding(handle, type_, scale, ids, tokens, table, ld_table, vocab, dim,
+                                 out, ld_out, stream or None)
+    if check:
+        _check(s, "spmm_embedding")
+    return s
+
+
+def spmm_embedding_grad(handle, type_, grad_type, scale, ids, tokens, dout, ld_dout, beta, dtable,
+                        ld_dtable, vocab, dim, stream=0, check=True) -> int:
+    """dtable = beta * dtable + the gradient of spmm_embedding."""
+    s = library().spmm_embedding_grad(handle, type_, grad_type, scale, ids, tokens, dout, ld_dout,
+                                      beta, dtable, ld_dtable, vocab, dim, stream or None)
+    if check:
+        _check(s, "spmm_embedding_grad")
+    return s
+
+
+def spmm_layer_norm(handle, type_, param_type, x, ldx, rows, dim, weight, bias, eps, y, ldy, mean,
+                    rstd, stream=0, check=True) -> int:
+    """y = (x - mean) * rstd * weight + bias for each row; mean and rstd are outputs."""
+    s = library().spmm_layer_norm(handle, type_, param_type, x, ldx, rows, dim, weight, bias, eps,
+                                  y, ldy, mean, rstd, stream or None)
+    if check:
+        _check(s, "spmm_layer_norm")
+    return s
+
+
+def spmm_layer_norm_grad(handle, type_, param_type, dy, ld_dy, x, ldx, mean, rstd, weight, rows,
+                         dim, dx, ld_dx, dweight, dbias, stream=0, check=True) -> int:
+    """Gradients of spmm_layer_norm with respect to x, weight and bias."""
+    s = library().spmm_layer_norm_grad(handle, type_, param_type, dy, ld_dy, x, ldx, mean, rstd,
+                                       weight, rows, dim, dx, ld_dx, dweight, dbias,
+                                       stream or None)
+    if check:
+        _check(s, "spmm_layer_norm_grad")
+    return s
+
+
+def spmm_token_logprob(handle, type_, alpha, logits, ld, rows, vocab, targets, top_k, logprob,
+                       entropy, lse, top_logprob, top_index, stream=0, check=True) -> int:
+    """Per row of logits: log probability of the target, entropy, log-sum-exp, alternatives."""
+    s = library().spmm_token_logprob(handle, type_, alpha, logits, ld, rows, vocab, targets,
+                                     top_k, logprob, entropy, lse, top_logprob, top_index,
+                                     stream or None)
+    if check:
+        _check(s, "spmm_token_logprob")
+    return s
+
+
+def spmm_token_logprob_grad(handle, type_, alpha, logits, ld, rows, vocab, targets, lse, entropy,
+                            dlogprob, dentropy, dlogits, ld_dlogits, stream=0, check=True) -> int:
+    """Gradient of the log probabilities and entropies with respect to the logits."""
+    s = library().spmm_token_logprob_grad(handle, type_, alpha, logits, ld, rows, vocab, targets,
+                                          lse, entropy, dlogprob, dentropy, dlogits, ld_dlogits,
+                                          stream or None)
+    if check:
+        _check(s, "spmm_token_logprob_grad")
     return s

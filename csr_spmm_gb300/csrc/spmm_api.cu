@@ -12,6 +12,7 @@
 
 #include "csr_spmm.h"
 #include "spmm_internal.h"
+#include "spmm_lm.h"
 #include "spmm_ops.h"
 
 using namespace spmm;
@@ -26,6 +27,8 @@ struct spmm_handle_s {
     size_t persist_prev = 0;          // the limit before, restored on destroy
     void* scratch = nullptr;
     size_t scratch_bytes = 0;
+    void* lm_scratch = nullptr;       // the language-model operators' own (spmm_lm_api.cu)
+    size_t lm_scratch_bytes = 0;
     int* check_status = nullptr;
     // occupancy cache of the rows kernel, keyed by (element size, W, G, R)
     struct OccEntry { int es, W, G, R, blocks; };
@@ -182,22 +185,27 @@ ScratchLayout layout_for(int64_t m, int64_t n, int es, int long_grid) {
 
 int long_grid_of(const spmm_handle_s* h) { return long_grid_for(h->num_sms); }
 
-spmm_status_t ensure_scratch(spmm_handle_s* h, size_t bytes) {
-    if (bytes <= h->scratch_bytes) return SPMM_OK;
-    if (h->scratch) {
+// Grow a device buffer of the handle to at least `bytes` (contents are lost).
+spmm_status_t grow(void** buf, size_t* have, size_t bytes) {
+    if (bytes <= *have) return SPMM_OK;
+    if (*buf) {
         cudaDeviceSynchronize();     // earlier calls may still use the old buffer
-        cudaFree(h->scratch);
-        h->scratch = nullptr;
-        h->scratch_bytes = 0;
+        cudaFree(*buf);
+        *buf = nullptr;
+        *have = 0;
     }
     const size_t want = align_up(bytes + bytes / 4, 1 << 20);
-    if (cudaMalloc(&h->scratch, want) != cudaSuccess) {
+    if (cudaMalloc(buf, want) != cudaSuccess) {
         cudaGetLastError();
-        h->scratch = nullptr;
+        *buf = nullptr;
         return SPMM_ERR_ALLOC;
     }
-    h->scratch_bytes = want;
+    *have = want;
     return SPMM_OK;
+}
+
+spmm_status_t ensure_scratch(spmm_handle_s* h, size_t bytes) {
+    return grow(&h->scratch, &h->scratch_bytes, bytes);
 }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -935,6 +943,26 @@ spmm_status_t plan_order_rows(spmm_plan_t pl, const int32_t* row_ptr, const int3
 
 }  // namespace
 
+namespace spmm {
+
+spmm_status_t lm_device(spmm_handle_t h, int* num_sms) {
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
+        cudaGetLastError();
+        return SPMM_ERR_INVALID_ARGUMENT;
+    }
+    *num_sms = h->num_sms;
+    return SPMM_OK;
+}
+
+spmm_status_t lm_scratch(spmm_handle_t h, size_t bytes, char** base) {
+    const spmm_status_t s = grow(&h->lm_scratch, &h->lm_scratch_bytes, bytes);
+    *base = static_cast<char*>(h->lm_scratch);
+    return s;
+}
+
+}  // namespace spmm
+
 extern "C" {
 
 spmm_status_t spmm_create(spmm_handle_t* out, int device) {
@@ -981,6 +1009,7 @@ spmm_status_t spmm_destroy(spmm_handle_t h) {
     for (auto& e : h->ev)
         if (e) cudaEventDestroy(e);
     if (h->scratch) cudaFree(h->scratch);
+    if (h->lm_scratch) cudaFree(h->lm_scratch);
     if (h->check_status) cudaFree(h->check_status);
     if (h->persist_bytes > 0) {
         cudaCtxResetPersistingL2Cache();

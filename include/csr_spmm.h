@@ -437,6 +437,132 @@ spmm_status_t spmm_csr_f32_noalloc(float alpha,
                                    const float *B, int64_t ldb, int64_t n,
                                    float beta, float *C, int64_t ldc, void *stream);
 
+/* ---- The two ends of a language model ----------------------------------------
+ * A language model's input table is read by a product with one stored entry
+ * per row (row t holds `scale` at column ids[t]); its gradient is the product
+ * of that matrix's transpose, whose rows (the tokens of one id) have
+ * power-law lengths.  Beside them stand the layer norm that takes the rows
+ * in, and the scan of the logits that gives the answer's log probabilities.
+ * The pages have no counterpart; these extend the library.
+ *
+ * Element types: every dense operand has one of the types below.  All sums,
+ * statistics and products are held in binary32 whatever the operands' type,
+ * and each result is rounded once, when it is stored.  Matrices are
+ * row-major with leading dimensions in elements, at least max(1, columns);
+ * any base address that suits the element type, and any leading dimension,
+ * is accepted (16-byte aligned rows are the fast case).  An output must not
+ * overlap an input unless the call says so.  Results are deterministic: no
+ * floating-point atomics, every sum in a fixed order.
+ *
+ * The calls are asynchronous on `stream`; the current device must be the
+ * handle's (SPMM_ERR_INVALID_ARGUMENT).  Scratch, where a call needs some, is
+ * the handle's own for these operators, grown with cudaMalloc (which
+ * synchronises the device): spmm_reserve_lm beforehand makes later calls
+ * free of allocation, as stream capture requires.  One stream at a time per
+ * handle, as for the products. */
+typedef enum { SPMM_F32 = 0, SPMM_F16 = 1, SPMM_BF16 = 2 } spmm_type_t;
+
+/* Grow the handle's scratch for gradients (spmm_embedding_grad with up to
+ * `rows` tokens, spmm_layer_norm_grad with up to `rows` rows) of up to `dim`
+ * columns.  Synchronous. */
+spmm_status_t spmm_reserve_lm(spmm_handle_t h, int64_t rows, int64_t dim);
+
+/* out[t, :] = scale * table[ids[t], :] for t < tokens (dim columns).
+ * An id outside [0, vocab) is padding: its row of out is zero.  scale == 0
+ * gives zeros without reading the table (the alpha == 0 rule).  table and out
+ * have type `type`; the product is formed in binary32 and rounded once.
+ * tokens == 0 or dim == 0: nothing is done.  table may be NULL only when
+ * vocab == 0 or scale == 0.  One launch, no scratch. */
+spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale,
+                             const int32_t *ids, int64_t tokens,
+                             const void *table, int64_t ld_table, int64_t vocab, int64_t dim,
+                             void *out, int64_t ld_out, void *stream);
+
+/* dtable[v, :] = beta * dtable[v, :] + scale * sum over t with ids[t] == v of
+ * dout[t, :], for every v < vocab: the gradient of spmm_embedding, added to
+ * what dtable holds.  beta == 0: dtable is write-only and rows without a token
+ * become zero; beta == 1: rows without a token are not touched.  Ids outside
+ * [0, vocab) take no part; scale == 0: dout and ids are not read.  dout has
+ * type `type`, dtable `grad_type`, which is `type` or SPMM_F32.  The tokens are
+ * sorted by id on the device (stable), and each row's sum is taken in binary32
+ * over pieces of consecutive sorted tokens whose bounds depend on `tokens`
+ * alone, then over the pieces in order.  Scratch: 16 bytes per token and at
+ * most 1/4 of the bytes of dout in binary32.  tokens <= 2^30. */
+spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t grad_type,
+                                  float scale, const int32_t *ids, int64_t tokens,
+                                  const void *dout, int64_t ld_dout, float beta,
+                                  void *dtable, int64_t ld_dtable, int64_t vocab, int64_t dim,
+                                  void *stream);
+
+/* y[r, :] = (x[r, :] - mean[r]) * rstd[r] * weight + bias for each of `rows`
+ * rows of dim columns, with mean[r] the row's mean and rstd[r] =
+ * 1 / sqrt(mean of the squared deviations + eps).  weight and bias (dim
+ * entries, either may be NULL: 1 and 0) have type `param_type`, which is
+ * `type` or SPMM_F32; mean and rstd are binary32 outputs for the gradient and
+ * may be NULL.  The deviations are taken from the row's own mean in a second
+ * pass over the row, so a row far from zero loses nothing.  y may be x.
+ * eps >= 0 (a constant row with eps == 0 gives NaN, as the formula does).
+ * rows == 0 or dim == 0: nothing is done.  One launch, no scratch. */
+spmm_status_t spmm_layer_norm(spmm_handle_t h, spmm_type_t type, spmm_type_t param_type,
+                              const void *x, int64_t ldx, int64_t rows, int64_t dim,
+                              const void *weight, const void *bias, float eps,
+                              void *y, int64_t ldy, float *mean, float *rstd, void *stream);
+
+/* Gradients of spmm_layer_norm.  With xhat = (x - mean) * rstd and
+ * g = dy * weight:
+ *   dx      = rstd * (g - rowmean(g) - xhat * rowmean(g * xhat))
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * dx has type `type` and may be dy; dweight and dbias have type `param_type`
+ * (either may be NULL: not computed) and are overwritten (zeros for
+ * rows == 0).  weight NULL means 1.  mean and rstd as spmm_layer_norm wrote
+ * them.  Scratch: at most 64 KB * dim, no more than 8 * rows * dim bytes. */
+spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t param_type,
+                                   const void *dy, int64_t ld_dy, const void *x, int64_t ldx,
+                                   const float *mean, const float *rstd, const void *weight,
+                                   int64_t rows, int64_t dim, void *dx, int64_t ld_dx,
+                                   void *dweight, void *dbias, void *stream);
+
+/* Log probabilities of given tokens.  With z = alpha * logits[r, :] (vocab
+ * columns; alpha > 0 is an inverse temperature) and p = softmax(z), per row:
+ *   lse         = log(sum(exp(z)))
+ *   logprob     = z[targets[r]] - lse, or 0 when targets[r] is outside
+ *                 [0, vocab) (a row without a target)
+ *   entropy     = -sum(p * log(p))
+ *   top_index   [rows, top_k] int32: the top_k largest logits, largest first,
+ *                 equal ones by lowest index;  top_logprob: their z - lse
+ * A logit of -inf is masked: p = 0 there, it adds nothing to the entropy, and
+ * it is never an alternative.  Alternatives that do not exist have index -1
+ * and log probability -inf.  A row without an unmasked logit (vocab == 0 too)
+ * has lse = -inf, entropy 0 and logprob -inf (0 without a target).  A NaN or
+ * +inf among the logits makes the row's lse, entropy, logprob and top_logprob
+ * NaN; NaNs are never alternatives.  The order of the alternatives is that of
+ * the logits themselves, before alpha.
+ * All outputs but top_index are binary32.  targets and logprob may be NULL
+ * together, entropy and lse each, top_logprob and top_index when top_k == 0.
+ * 0 <= top_k <= 32.  One pass over the logits, one launch, no scratch. */
+#define SPMM_TOP_MAX 32
+spmm_status_t spmm_token_logprob(spmm_handle_t h, spmm_type_t type, float alpha,
+                                 const void *logits, int64_t ld, int64_t rows, int64_t vocab,
+                                 const int32_t *targets, int32_t top_k, float *logprob,
+                                 float *entropy, float *lse, float *top_logprob,
+                                 int32_t *top_index, void *stream);
+
+/* Gradient of spmm_token_logprob's logprob and entropy with respect to the
+ * logits.  With q = alpha * logits - lse and p = exp(q):
+ *   dlogits = alpha * (dlogprob * (onehot(target) - p)
+ *                      - dentropy * p * (q + entropy))
+ * lse and entropy as spmm_token_logprob wrote them.  A row without a target
+ * has no dlogprob term; masked logits (p = 0) get no entropy term; a row whose
+ * lse is -inf gets zeros.  targets and dlogprob may be NULL together, dentropy
+ * and entropy together.  dlogits has type `type` and may be logits.  One launch,
+ * no scratch. */
+spmm_status_t spmm_token_logprob_grad(spmm_handle_t h, spmm_type_t type, float alpha,
+                                      const void *logits, int64_t ld, int64_t rows,
+                                      int64_t vocab, const int32_t *targets, const float *lse,
+                                      const float *entropy, const float *dlogprob,
+                                      const float *dentropy, void *dlogits, int64_t ld_dlogits,
+                                      void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *spmm_status_string(spmm_status_t s);
 
