@@ -7,6 +7,7 @@
 // stable order, and the sums below have a fixed order.
 #include <algorithm>
 
+#include "spmm_internal.h"
 #include "spmm_lm_device.cuh"
 
 namespace spmm {
@@ -57,8 +58,9 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int n
         for (int u = 0; u < EMBED_BATCH; ++u) {
             if (to[u] < 0) continue;
             float f[W];
+            unpack(v[u], f);
 #pragma unroll
-            for (int i = 0; i < W; ++i) f[i] = valid[u] ? p.scale * to_f32(v[u].v[i]) : 0.0f;
+            for (int i = 0; i < W; ++i) f[i] = valid[u] ? p.scale * f[i] : 0.0f;
             store_vec<Cache::STREAM, T, W>(out + to[u], f);
         }
     }
@@ -85,11 +87,16 @@ constexpr unsigned NO_ID = 0xffffffffu;
 
 // Sorts each tile of SORT_TILE tokens: a bitonic network on the 64-bit keys
 // in shared memory.  Ids outside [0, vocab) get the largest key and end up
-// behind every row.  Pairs at distance <= 32 stay within one warp's 64 keys,
+// behind every row.  Also zeroes the sums' arrival counters.  Pairs at distance <= 32 stay within one warp's 64 keys,
 // so those steps need no block barrier.
 __global__ __launch_bounds__(SORT_THREADS) void sort_tiles(const int* ids, int tokens,
-                                                           int64_t vocab, uint64_t* keys) {
+                                                           int64_t vocab, uint64_t* keys,
+                                                           int* arrived, int64_t counters) {
     __shared__ uint64_t s[SORT_TILE];
+    allow_successor();
+    for (int64_t i = (int64_t)blockIdx.x * SORT_THREADS + threadIdx.x; i < counters;
+         i += (int64_t)gridDim.x * SORT_THREADS)
+        arrived[i] = 0;
     const int t0 = blockIdx.x * SORT_TILE;
     const int n = min(SORT_TILE, tokens - t0);
     int np = 64;
@@ -143,6 +150,8 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
 // its own index plus the count of smaller keys in the other runs.
 __global__ __launch_bounds__(256) void merge_runs(const uint64_t* in, uint64_t* out, int tokens,
                                                   int64_t run) {
+    allow_successor();
+    wait_for_predecessor();
     const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (g >= tokens) return;
     const uint64_t key = in[g];
@@ -160,27 +169,249 @@ __global__ __launch_bounds__(256) void merge_runs(const uint64_t* in, uint64_t* 
 
 // ---- gradient: sums --------------------------------------------------------------
 
-// One warp per table row.
-template <typename T, typename G>
-__global__ __launch_bounds__(256) void grad_rows(EmbedGradParams p, const uint64_t* keys) {
-    const int lane = threadIdx.x & 31;
-    const T* dout = static_cast<const T*>(p.dout);
-    G* dtable = static_cast<G*>(p.dtable);
-    const int64_t warps = (int64_t)gridDim.x * 8;
-    for (int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); v < p.vocab; v += warps) {
-        const int a = count_below(keys, (int)p.tokens, (uint64_t)v << 32);
-        const int b = count_below(keys, (int)p.tokens, (uint64_t)(v + 1) << 32);
-        if (a == b && p.beta == 1.0f) continue;
-        for (int64_t c = lane; c < p.dim; c += 32) {
-            float sum = 0.0f;
-            for (int i = a; i < b; ++i)
-                sum += to_f32(dout[(int64_t)(unsigned)keys[i] * p.ld_dout + c]);
-            sum *= p.scale;
-            G* at = dtable + v * p.ld_dtable + c;
-            if (p.beta != 0.0f) sum += p.beta * to_f32(*at);
-            *at = from_f32<G>(sum);
+// The sorted tokens are cut into pieces of equal length; a warp sums one piece
+// over one panel of columns, reading each token's row segment once.  A run of
+// one id that lies within the piece is complete and goes to its table row; a
+// run that crosses the piece's bounds leaves a partial sum, and the last of the
+// run's pieces to arrive adds the run's partials in piece order.
+constexpr int PANEL = 256;           // columns per warp: 512 bytes of a 16-bit row
+constexpr int PIECE_MIN = 8, PIECE_MAX = 256;
+
+// Tokens per piece: as many as leave about 16384 warps of work (three to four
+// times what the SMs hold at once), so that few runs are cut.  It depends on the
+// call's sizes only, so the order of every sum does too.
+inline int64_t panels_of(int64_t dim) { return (dim + PANEL - 1) / PANEL; }
+inline int piece_of(int64_t tokens, int64_t dim) {
+    int piece = PIECE_MIN;
+    while (piece < PIECE_MAX && tokens * panels_of(dim) / piece > 16384) piece *= 2;
+    return piece;
+}
+inline int64_t padded(int64_t dim) { return (dim + 7) / 8 * 8; }   // partial rows: 32 bytes
+
+struct GradWork {
+    const uint64_t* keys;            // sorted
+    float* partials;                 // [pieces][2][padded dim]: run from before, run to the next
+    int* arrived;                    // [pieces][panels], zeroed by sort_tiles
+    int64_t dim_padded;
+    int piece;
+    int panels;
+    int64_t sum_items;               // pieces * panels warps sum; the rest fill
+    int fill_rows;                   // table rows per filling warp
+};
+
+// Number of keys below `key`, by the whole warp: 32 probes per step.
+__device__ __forceinline__ int warp_count_below(const uint64_t* a, int n, uint64_t key, int lane) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int step = (hi - lo) / 32 + 1;
+        const int64_t at = lo + (int64_t)lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < hi && a[at] < key);
+        const int k = __popc(below);
+        if (k == 0) return lo;
+        hi = (int)min((int64_t)hi, lo + (int64_t)k * step);
+        lo += (k - 1) * step + 1;
+    }
+    return lo;
+}
+
+// W elements per access, V accesses per lane and row segment: W * V * 32 == PANEL.
+template <typename T, typename G, int W, int V, int BATCH>
+struct GradSum {
+    static_assert(W * V * 32 == PANEL);
+    const EmbedGradParams& p;
+    const GradWork& k;
+    int lane;
+    int64_t col;                     // the panel's first column
+    float acc[V][W];
+
+    __device__ bool inside(int v) const { return col + (v * 32 + lane) * W < p.dim; }
+    __device__ void clear() {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[v][i] = 0.0f;
+    }
+    // dtable[row] = beta * dtable[row] + scale * acc
+    __device__ void finish(unsigned row) {
+        G* to = static_cast<G*>(p.dtable) + (int64_t)row * p.ld_dtable + col + lane * W;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (!inside(v)) continue;
+            float f[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) f[i] = p.scale * acc[v][i];
+            if (p.beta != 0.0f) {
+                float old[W];
+                unpack(load_vec<Cache::STREAM, G, W>(to + v * 32 * W), old);
+#pragma unroll
+                for (int i = 0; i < W; ++i) f[i] += p.beta * old[i];
+            }
+            store_vec<Cache::STREAM, G, W>(to + v * 32 * W, f);
         }
     }
+    __device__ float* partial(int64_t slot) const {
+        return k.partials + slot * k.dim_padded + col + lane * W;
+    }
+    // Keep the sum of a run that crosses the piece's bounds.
+    __device__ void leave_partial(int64_t piece, bool from_before) {
+        float* to = partial(2 * piece + (from_before ? 0 : 1));
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (inside(v)) store_vec<Cache::KEEP, float, W>(to + v * 32 * W, acc[v]);
+    }
+    // This piece's part of the run of `id` is kept: the last piece to come here
+    // adds the parts in piece order.
+    __device__ void join(unsigned id, int panel) {
+        const int n = (int)p.tokens;
+        const int a = warp_count_below(k.keys, n, (uint64_t)id << 32, lane);
+        const int b = warp_count_below(k.keys, n, (uint64_t)(id + 1) << 32, lane);
+        const int64_t first = a / k.piece, last = (b - 1) / k.piece;
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(k.arrived + first * k.panels + panel, 1);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before != last - first) return;
+        __threadfence();
+        clear();
+        for (int64_t q = first; q <= last; q += 4) {
+            float got[4][V][W];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        got[u][v][i] = q + u <= last && inside(v)
+                                           ? __ldcg(partial(2 * (q + u) + (q + u == first ? 1 : 0)) +
+                                                    v * 32 * W + i)
+                                           : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) acc[v][i] += got[u][v][i];
+        }
+        finish(id);
+    }
+
+    __device__ void sum(int64_t piece, int panel) {
+        const T* dout = static_cast<const T*>(p.dout) + col + lane * W;
+        const int s0 = (int)(piece * k.piece);
+        const int s1 = (int)min((int64_t)s0 + k.piece, p.tokens);
+        unsigned run = (unsigned)(k.keys[s0] >> 32);            // the id being summed
+        if (run == NO_ID) return;
+        bool from_before = s0 > 0 && (unsigned)(k.keys[s0 - 1] >> 32) == run;
+        unsigned head = NO_ID;                                  // a run from before that ended
+        clear();
+        for (int base = s0; base < s1; base += 32) {
+            const uint64_t mine = base + lane < s1 ? k.keys[base + lane] : ~0ull;
+            const unsigned id_l = (unsigned)(mine >> 32), pos_l = (unsigned)mine;
+            const int live = __popc(__ballot_sync(0xffffffffu, id_l != NO_ID));  // a prefix
+            for (int j = 0; j < live; j += BATCH) {
+                Vec<T, W> x[BATCH][V];
+#pragma unroll
+                for (int u = 0; u < BATCH; ++u) {
+                    const int64_t row = __shfl_sync(0xffffffffu, pos_l, (j + u) & 31);
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (j + u < live && inside(v))
+                            x[u][v] = load_vec<Cache::STREAM, T, W>(dout + row * p.ld_dout +
+                                                                    v * 32 * W);
+                }
+#pragma unroll
+                for (int u = 0; u < BATCH; ++u) {
+                    const unsigned id = __shfl_sync(0xffffffffu, id_l, (j + u) & 31);
+                    if (j + u >= live) break;
+                    if (id != run) {                            // the run before ends here
+                        if (from_before) {
+                            leave_partial(piece, true);
+                            head = run;
+                            from_before = false;
+                        } else {
+                            finish(run);
+                        }
+                        clear();
+                        run = id;
+                    }
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float f[W];
+                        unpack(x[u][v], f);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) acc[v][i] += f[i];
+                    }
+                }
+            }
+            if (live < 32) break;
+        }
+        const bool goes_on = s1 < p.tokens && (unsigned)(k.keys[s1] >> 32) == run;
+        const bool crosses = from_before || goes_on;
+        if (crosses) leave_partial(piece, from_before);
+        else finish(run);
+        if (head != NO_ID) join(head, panel);
+        if (crosses) join(run, panel);
+    }
+};
+
+// Rows without a token: beta * dtable, zeros for beta == 0.
+template <typename G, int W>
+__device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t item, int lane) {
+    const int64_t v0 = item * k.fill_rows;
+    const int rows = (int)min((int64_t)k.fill_rows, p.vocab - v0);
+    bool absent = false;
+    if (lane < rows) {
+        const uint64_t key = (uint64_t)(v0 + lane) << 32;
+        const int at = count_below(k.keys, (int)p.tokens, key);
+        absent = at == p.tokens || k.keys[at] >> 32 != key >> 32;
+    }
+    const unsigned todo = __ballot_sync(0xffffffffu, absent);
+    for (int r = 0; r < rows; ++r) {
+        if (!(todo >> r & 1)) continue;
+        G* to = static_cast<G*>(p.dtable) + (v0 + r) * p.ld_dtable;
+        for (int64_t c = lane * W; c < p.dim; c += 32 * W) {
+            float f[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) f[i] = 0.0f;
+            if (p.beta != 0.0f) {
+                unpack(load_vec<Cache::STREAM, G, W>(to + c), f);
+#pragma unroll
+                for (int i = 0; i < W; ++i) f[i] *= p.beta;
+            }
+            store_vec<Cache::STREAM, G, W>(to + c, f);
+        }
+    }
+}
+
+template <typename T, typename G, int W, int V, int BATCH>
+__global__ __launch_bounds__(256) void grad_sums(EmbedGradParams p, GradWork k) {
+    wait_for_predecessor();
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (item < k.sum_items) {
+        const int panel = (int)(item % k.panels);
+        GradSum<T, G, W, V, BATCH> s{p, k, lane, (int64_t)panel * PANEL};
+        s.sum(item / k.panels, panel);
+    } else {
+        const int64_t fill = item - k.sum_items;
+        if (fill * k.fill_rows < p.vocab) fill_rows<G, W>(p, k, fill, lane);
+    }
+}
+
+struct GradLayout {
+    size_t keys, other, arrived, partials, total;
+};
+GradLayout grad_layout(int64_t tokens, int64_t dim) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const int piece = piece_of(tokens, dim);
+    const size_t pieces = (size_t)((tokens + piece - 1) / piece);
+    GradLayout l{};
+    l.other = up((size_t)tokens * 8);
+    l.arrived = l.other + up((size_t)tokens * 8);
+    l.partials = l.arrived + up(pieces * (size_t)panels_of(dim) * sizeof(int));
+    l.total = l.partials + up(pieces * 2 * (size_t)padded(dim) * sizeof(float));
+    return l;
 }
 
 }  // namespace
@@ -196,32 +427,58 @@ cudaError_t launch_embedding(spmm_type_t type, const EmbedParams& p, int num_sms
     });
 }
 
-size_t embed_grad_scratch(int64_t tokens, int64_t dim) {
-    (void)dim;
-    return (size_t)tokens * 16;
-}
+size_t embed_grad_scratch(int64_t tokens, int64_t dim) { return grad_layout(tokens, dim).total; }
 
 cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
                                   const EmbedGradParams& p, char* scratch, int num_sms,
                                   cudaStream_t st) {
+    (void)num_sms;
+    const GradLayout l = grad_layout(p.tokens, p.dim);
     uint64_t* keys = reinterpret_cast<uint64_t*>(scratch);
-    uint64_t* other = keys + p.tokens;
+    uint64_t* other = reinterpret_cast<uint64_t*>(scratch + l.other);
+    GradWork k{};
+    k.arrived = reinterpret_cast<int*>(scratch + l.arrived);
+    k.partials = reinterpret_cast<float*>(scratch + l.partials);
+    k.dim_padded = padded(p.dim);
+    k.piece = piece_of(p.tokens, p.dim);
+    k.panels = (int)panels_of(p.dim);
+    k.sum_items = (p.tokens + k.piece - 1) / k.piece * k.panels;
+    // a filling warp writes about 32 KB when no row of its share has a token
+    const int64_t row_bytes = p.dim * lm_elem_size(grad_type);
+    k.fill_rows = (int)std::min<int64_t>(32, std::max<int64_t>(1, 32768 / row_bytes));
+    const int64_t fill_items =
+        p.beta == 1.0f ? 0 : (p.vocab + k.fill_rows - 1) / k.fill_rows;
     if (p.tokens > 0) {
         const int tiles = (int)((p.tokens + SORT_TILE - 1) / SORT_TILE);
-        sort_tiles<<<tiles, SORT_THREADS, 0, st>>>(p.ids, (int)p.tokens, p.vocab, keys);
-        for (int64_t run = SORT_TILE; run < p.tokens; run *= MERGE_WAYS) {
-            merge_runs<<<(unsigned)((p.tokens + 255) / 256), 256, 0, st>>>(keys, other,
-                                                                         (int)p.tokens, run);
+        sort_tiles<<<tiles, SORT_THREADS, 0, st>>>(p.ids, (int)p.tokens, p.vocab, keys, k.arrived,
+                                                   k.sum_items);
+        cudaError_t e = cudaGetLastError();
+        for (int64_t run = SORT_TILE; e == cudaSuccess && run < p.tokens; run *= MERGE_WAYS) {
+            e = launch_chained(merge_runs, dim3((unsigned)((p.tokens + 255) / 256)), dim3(256), 0,
+                               st, true, (const uint64_t*)keys, other, (int)p.tokens, run);
             std::swap(keys, other);
         }
+        if (e != cudaSuccess) return e;
     }
-    const unsigned blocks = (unsigned)std::min<int64_t>((p.vocab + 7) / 8, num_sms * 8);
+    k.keys = keys;
+    const int64_t blocks = (k.sum_items + fill_items + 7) / 8;
+    if (blocks == 0) return cudaSuccess;
     const bool same = type == grad_type;
     return with_type(type, [&](auto t) {
         using T = decltype(t);
-        if (same) grad_rows<T, T><<<blocks, 256, 0, st>>>(p, keys);
-        else grad_rows<T, float><<<blocks, 256, 0, st>>>(p, keys);
-        return cudaGetLastError();
+        constexpr int W = 16 / sizeof(T);
+        auto run = [&](auto kernel) {
+            return launch_chained(kernel, dim3((unsigned)blocks), dim3(256), 0, st, p.tokens > 0,
+                                  p, k);
+        };
+        const bool wide = p.dim % W == 0 &&
+                          rows_aligned16(p.dtable, p.ld_dtable, lm_elem_size(grad_type)) &&
+                          (p.tokens == 0 || rows_aligned16(p.dout, p.ld_dout, sizeof(T)));
+        if (same)
+            return wide ? run(grad_sums<T, T, W, PANEL / 32 / W, W>)
+                        : run(grad_sums<T, T, 1, PANEL / 32, 4>);
+        return wide ? run(grad_sums<T, float, W, PANEL / 32 / W, W>)
+                    : run(grad_sums<T, float, 1, PANEL / 32, 4>);
     });
 }
 

@@ -24,48 +24,97 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(x);
 }
 
-// W consecutive elements, moved with one access.
+// W consecutive elements as they lie in memory: W > 1 in 32-bit words, so that
+// 16-bit elements stay packed in registers until they are used.
 template <typename T, int W>
-struct alignas(sizeof(T) * W) Vec {
-    T v[W];
+struct Vec {
+    static constexpr int WORDS = (int)sizeof(T) * W / 4;
+    uint32_t w[WORDS];
 };
+template <typename T>
+struct Vec<T, 1> {
+    T w;
+};
+
+__device__ __forceinline__ void unpack_word(uint32_t w, float* f, __nv_bfloat16) {
+    f[0] = __uint_as_float(w << 16);
+    f[1] = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_word(uint32_t w, float* f, __half) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    f[0] = x.x;
+    f[1] = x.y;
+}
+__device__ __forceinline__ uint32_t pack_word(const float* f, __nv_bfloat16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t pack_word(const float* f, __half) {
+    const __half2 x = __floats2half2_rn(f[0], f[1]);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// The elements of a Vec in binary32.
+template <typename T, int W>
+__device__ __forceinline__ void unpack(const Vec<T, W>& r, float (&f)[W]) {
+    if constexpr (W == 1) {
+        f[0] = to_f32(r.w);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) f[i] = __uint_as_float(r.w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) unpack_word(r.w[i], f + 2 * i, T{});
+    }
+}
 
 // How a load treats the caches: KEEP for what is read again, STREAM for what
 // is read once.
 enum class Cache { KEEP, STREAM };
 
+// W consecutive elements: 16-byte accesses when W > 1, one element otherwise.
 template <Cache C, typename T, int W>
 __device__ __forceinline__ Vec<T, W> load_vec(const T* p) {
     Vec<T, W> r;
-    if constexpr (sizeof(T) * W == 16) {
-        const int4 u = C == Cache::STREAM ? __ldcs(reinterpret_cast<const int4*>(p))
-                                          : *reinterpret_cast<const int4*>(p);
-        r = *reinterpret_cast<const Vec<T, W>*>(&u);
+    if constexpr (W > 1) {
+        static_assert(sizeof(T) * W % 16 == 0);
+        const uint4* from = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+        for (int i = 0; i < Vec<T, W>::WORDS / 4; ++i) {
+            const uint4 u = C == Cache::STREAM ? __ldcs(from + i) : from[i];
+            r.w[4 * i] = u.x;
+            r.w[4 * i + 1] = u.y;
+            r.w[4 * i + 2] = u.z;
+            r.w[4 * i + 3] = u.w;
+        }
     } else {
-        static_assert(W == 1);
-        r.v[0] = C == Cache::STREAM ? __ldcs(p) : *p;
+        r.w = C == Cache::STREAM ? __ldcs(p) : *p;
     }
     return r;
 }
 
-// Store W floats rounded to T.  W * sizeof(T) is 16 or 32 bytes (one or two
-// accesses), or one element.
+// Store W floats rounded to T, with the same accesses.
 template <Cache C, typename T, int W>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[W]) {
-    Vec<T, W> r;
-#pragma unroll
-    for (int i = 0; i < W; ++i) r.v[i] = from_f32<T>(f[i]);
     if constexpr (W > 1) {
         static_assert(sizeof(T) * W % 16 == 0);
-        const int4* u = reinterpret_cast<const int4*>(&r);
+        uint32_t w[Vec<T, W>::WORDS];
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) * W / 16); ++i) {
-            if (C == Cache::STREAM) __stcs(reinterpret_cast<int4*>(p) + i, u[i]);
-            else reinterpret_cast<int4*>(p)[i] = u[i];
+        for (int i = 0; i < Vec<T, W>::WORDS; ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+            else w[i] = pack_word(f + 2 * i, T{});
+        }
+        uint4* to = reinterpret_cast<uint4*>(p);
+#pragma unroll
+        for (int i = 0; i < Vec<T, W>::WORDS / 4; ++i) {
+            const uint4 u = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            if (C == Cache::STREAM) __stcs(to + i, u);
+            else to[i] = u;
         }
     } else {
-        if (C == Cache::STREAM) __stcs(p, r.v[0]);
-        else *p = r.v[0];
+        const T v = from_f32<T>(f[0]);
+        if (C == Cache::STREAM) __stcs(p, v);
+        else *p = v;
     }
 }
 
