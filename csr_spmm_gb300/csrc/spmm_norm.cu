@@ -6,6 +6,7 @@
 // mean far from zero.
 #include <algorithm>
 
+#include "spmm_internal.h"
 #include "spmm_lm_device.cuh"
 
 namespace spmm {
@@ -13,6 +14,7 @@ namespace spmm {
 namespace {
 
 constexpr int NORM_THREADS = 256;
+constexpr int NORM_GRAD_THREADS = 512;   // the gradient's block: up to 128 registers a thread
 
 // Sum over the block (every thread gets it); `s` holds one float per warp.
 template <int THREADS>
@@ -30,6 +32,102 @@ __device__ __forceinline__ float block_sum(float x, float* s) {
 template <typename P>
 __device__ __forceinline__ float param(const void* p, int64_t i, float none) {
     return p ? to_f32(static_cast<const P*>(p)[i]) : none;
+}
+
+// W parameters from column c, or the value `none` where there are none.
+template <typename P, int W>
+__device__ __forceinline__ void params(const void* p, int64_t c, float none, float (&f)[W]) {
+    if (p) {
+        unpack(load_vec<Cache::KEEP, P, W>(static_cast<const P*>(p) + c), f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) f[i] = none;
+    }
+}
+
+// Barrier of one row's warps (barrier 0 is the block's own).
+__device__ __forceinline__ void row_barrier(int row, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "r"(threads) : "memory");
+}
+
+// Sum over a row's `warps` warps, in warp order; `s` has a slot for each.
+__device__ __forceinline__ float row_sum(float x, float* s, int row, int warps) {
+    x = warp_sum(x);
+    if (warps == 1) return x;
+    if ((threadIdx.x & 31) == 0) s[(threadIdx.x >> 5) % warps] = x;
+    row_barrier(row, warps * 32);
+    float t = 0.0f;
+    for (int i = 0; i < warps; ++i) t += s[i];
+    return t;
+}
+
+// The row in registers: `warps` warps hold it in K accesses of W elements per
+// lane, so x is read once and the second pass over it costs no memory.  Several
+// narrow rows share a block.  The bound is HBM (read x, write y).
+template <typename T, typename P, int W, int K>
+__global__ __launch_bounds__(1024) void norm_rows(NormParams p, int warps, int nvec) {
+    __shared__ float s[2][32];
+    const int threads = warps * 32;
+    const int in_block = threadIdx.x / threads, tid = threadIdx.x % threads;
+    const int64_t r = (int64_t)blockIdx.x * (blockDim.x / threads) + in_block;
+    if (r >= p.rows) return;
+    const T* x = static_cast<const T*>(p.x) + r * p.ldx;
+    Vec<T, W> held[K];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (k * threads + tid < nvec)
+            held[k] = load_vec<Cache::STREAM, T, W>(x + (int64_t)(k * threads + tid) * W);
+    // one access per lane is the case of few rows, where latency counts: the
+    // parameters are on their way during the sums
+    float w0[W], b0[W];
+    if constexpr (K == 1)
+        if (tid < nvec) {
+            params<P, W>(p.weight, tid * W, 1.0f, w0);
+            params<P, W>(p.bias, tid * W, 0.0f, b0);
+        }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (k * threads + tid < nvec) {
+            float f[W];
+            unpack(held[k], f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum += f[i];
+        }
+    float* slot = s[0] + in_block * warps;
+    const float mean = row_sum(sum, slot, in_block, warps) / (float)p.dim;
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (k * threads + tid < nvec) {
+            float f[W];
+            unpack(held[k], f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum += (f[i] - mean) * (f[i] - mean);
+        }
+    slot = s[1] + in_block * warps;
+    const float var = row_sum(sum, slot, in_block, warps) / (float)p.dim;
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+    T* y = static_cast<T*>(p.y) + r * p.ldy;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int at = k * threads + tid;
+        if (at >= nvec) continue;
+        float f[W], w[W], b[W];
+        unpack(held[k], f);
+        if constexpr (K > 1) {
+            params<P, W>(p.weight, at * W, 1.0f, w);
+            params<P, W>(p.bias, at * W, 0.0f, b);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            f[i] = (f[i] - mean) * rstd * (K == 1 ? w0[i] : w[i]) + (K == 1 ? b0[i] : b[i]);
+        store_vec<Cache::STREAM, T, W>(y + (int64_t)at * W, f);
+    }
+    if (tid == 0) {
+        if (p.mean) p.mean[r] = mean;
+        if (p.rstd) p.rstd[r] = rstd;
+    }
 }
 
 // Any width and alignment: a block per row, the row read again for each pass.
@@ -55,6 +153,113 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_any(NormParams p) {
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[r] = mean;
             if (p.rstd) p.rstd[r] = rstd;
+        }
+    }
+}
+
+// dx, and this block's share of dweight and dbias, in one pass over dy and x: a
+// row's `warps` warps hold it in registers, walk the rows with a fixed stride
+// (the next row's accesses are issued before this row's sums), and keep their
+// columns' sums of dy * xhat and dy in registers to the end.  The bound is HBM
+// (read dy and x, write dx).  part: [slices][2][dim].
+template <typename T, typename P, int W, int K>
+__global__ __launch_bounds__(NORM_GRAD_THREADS) void norm_grad_rows(NormGradParams p, int warps,
+                                                                    int nvec, int slices) {
+    __shared__ float s[2][2][32];
+    const int threads = warps * 32;
+    const int in_block = threadIdx.x / threads, tid = threadIdx.x % threads;
+    const int slice = blockIdx.x * (blockDim.x / threads) + in_block;
+    if (slice >= slices) return;
+    const T* xs = static_cast<const T*>(p.x);
+    const T* dys = static_cast<const T*>(p.dy);
+    const bool sums = p.dweight || p.dbias;
+    // 16 elements a lane leave no registers for the weights in binary32 (W = 4) and
+    // for single accesses (W = 1): those read them again for each row, from L1
+    constexpr bool HOLD = W * K < 16 || W == 8;
+    Vec<T, W> x[K], dy[K];
+    float weight[HOLD ? K : 1][W], dw[K][W], db[K][W];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int at = k * threads + tid;
+            if (at < nvec) {
+                x[k] = load_vec<Cache::STREAM, T, W>(xs + r * p.ldx + (int64_t)at * W);
+                dy[k] = load_vec<Cache::STREAM, T, W>(dys + r * p.ld_dy + (int64_t)at * W);
+            }
+        }
+    };
+    fetch(slice);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) dw[k][i] = db[k][i] = 0.0f;
+        if (HOLD && k * threads + tid < nvec)
+            params<P, W>(p.weight, (int64_t)(k * threads + tid) * W, 1.0f, weight[HOLD ? k : 0]);
+    }
+    int turn = 0;
+    for (int64_t r = slice; r < p.rows; r += slices) {
+        const float mean = p.mean[r], rstd = p.rstd[r];
+        float xh[K][W], g[K][W];
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (k * threads + tid < nvec) {
+                unpack(x[k], xh[k]);
+                unpack(dy[k], g[k]);
+                float (&wk)[W] = weight[HOLD ? k : 0];
+                if (!HOLD) params<P, W>(p.weight, (int64_t)(k * threads + tid) * W, 1.0f, wk);
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    xh[k][i] = (xh[k][i] - mean) * rstd;
+                    dw[k][i] += g[k][i] * xh[k][i];
+                    db[k][i] += g[k][i];
+                    g[k][i] *= wk[i];
+                    a += g[k][i];
+                    b += g[k][i] * xh[k][i];
+                }
+            }
+        if (r + slices < p.rows) fetch(r + slices);
+        a = warp_sum(a);
+        b = warp_sum(b);
+        if (warps > 1) {
+            // two sets of slots in turn: one barrier per row keeps them apart
+            float* sa = s[turn][0] + in_block * warps;
+            float* sb = s[turn][1] + in_block * warps;
+            turn ^= 1;
+            if ((threadIdx.x & 31) == 0) {
+                sa[tid >> 5] = a;
+                sb[tid >> 5] = b;
+            }
+            row_barrier(in_block, threads);
+            a = b = 0.0f;
+            for (int i = 0; i < warps; ++i) {
+                a += sa[i];
+                b += sb[i];
+            }
+        }
+        a /= (float)p.dim;
+        b /= (float)p.dim;
+        T* dx = static_cast<T*>(p.dx) + r * p.ld_dx;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int at = k * threads + tid;
+            if (at >= nvec) continue;
+#pragma unroll
+            for (int i = 0; i < W; ++i) g[k][i] = rstd * (g[k][i] - a - xh[k][i] * b);
+            store_vec<Cache::STREAM, T, W>(dx + (int64_t)at * W, g[k]);
+        }
+    }
+    allow_successor();
+    if (!sums) return;
+    float* part = p.part + (int64_t)slice * 2 * p.dim;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int at = k * threads + tid;
+        if (at >= nvec) continue;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            part[(int64_t)at * W + i] = dw[k][i];
+            part[p.dim + (int64_t)at * W + i] = db[k][i];
         }
     }
 }
@@ -113,59 +318,146 @@ __global__ __launch_bounds__(256) void norm_dw_any(NormGradParams p) {
     }
 }
 
-// dweight and dbias from the slices' partial sums, added in slice order.
+// dweight and dbias from the slices' partial sums: a block takes 32 columns, each
+// of its warps every 8th slice in order, then the warps' sums are added in order.
 template <typename P>
 __global__ __launch_bounds__(256) void norm_dw_join(NormGradParams p, int slices) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * p.dim) return;
-    const int which = i >= p.dim;
-    const int64_t c = i - which * p.dim;
+    __shared__ float s[8][32];
+    wait_for_predecessor();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int which = blockIdx.y;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     P* out = static_cast<P*>(which ? p.dbias : p.dweight);
     if (!out) return;
     float t = 0.0f;
-    for (int k = 0; k < slices; ++k) t += p.part[((int64_t)k * 2 + which) * p.dim + c];
+    if (c < p.dim) {
+        const float* part = p.part + which * p.dim + c;
+#pragma unroll 8
+        for (int k = w; k < slices; k += 8) t += part[(int64_t)k * 2 * p.dim];
+    }
+    s[w][lane] = t;
+    __syncthreads();
+    if (w > 0 || c >= p.dim) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += s[i][lane];
     out[c] = from_f32<P>(t);
 }
 
-int64_t slices_of(int64_t rows) { return (rows + SLICE_ROWS - 1) / SLICE_ROWS; }
+int64_t slices_any(int64_t rows) { return (rows + SLICE_ROWS - 1) / SLICE_ROWS; }
+
+// Warps that hold a row of nvec accesses, K per lane.
+int warps_for(int64_t nvec, int K) {
+    int warps = 1;
+    while ((int64_t)warps * 32 * K < nvec) warps *= 2;
+    return warps;
+}
+
+// Slices of the register kernel's grid: one row at a time each, as many as the
+// SMs hold at NORM_GRAD_THREADS threads per SM.
+int64_t slices_rows(int64_t rows, int warps, int num_sms) {
+    return std::min<int64_t>(rows, (int64_t)num_sms * (NORM_GRAD_THREADS / 32) / warps);
+}
+
+template <typename T, typename P, int W, int K>
+cudaError_t norm_launch(const NormParams& p, cudaStream_t st) {
+    const int nvec = (int)(p.dim / W);
+    const int warps = warps_for(nvec, K);
+    const int rows = std::max(1, 8 / warps);          // at least 256 threads
+    norm_rows<T, P, W, K><<<(unsigned)((p.rows + rows - 1) / rows), rows * warps * 32, 0, st>>>(
+        p, warps, nvec);
+    return cudaGetLastError();
+}
+
+template <typename T, typename P, int W, int K>
+cudaError_t norm_grad_launch(const NormGradParams& p, int num_sms, cudaStream_t st, int* slices) {
+    const int nvec = (int)(p.dim / W);
+    const int warps = warps_for(nvec, K);
+    const int rows = std::max(1, 4 / warps);          // at least 128 threads
+    *slices = (int)slices_rows(p.rows, warps, num_sms);
+    norm_grad_rows<T, P, W, K><<<(*slices + rows - 1) / rows, rows * warps * 32, 0, st>>>(
+        p, warps, nvec, *slices);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
 cudaError_t launch_layer_norm(spmm_type_t type, spmm_type_t param_type, const NormParams& p,
                               int num_sms, cudaStream_t st) {
-    const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
-    return with_type(type, [&](auto t) {
+    auto typed = [&](auto t, auto pt) {
         using T = decltype(t);
-        if (type == param_type) norm_any<T, T><<<blocks, NORM_THREADS, 0, st>>>(p);
-        else norm_any<T, float><<<blocks, NORM_THREADS, 0, st>>>(p);
+        using P = decltype(pt);
+        constexpr int W = 16 / sizeof(T);
+        const bool wide = p.dim % W == 0 && rows_aligned16(p.x, p.ldx, sizeof(T)) &&
+                          rows_aligned16(p.y, p.ldy, sizeof(T)) &&
+                          (!p.weight || rows_aligned16(p.weight, 0, 1)) &&
+                          (!p.bias || rows_aligned16(p.bias, 0, 1));
+        // A row takes at most 1024 threads.  Few rows leave SMs idle: then the
+        // most threads per row (one access each) give the shortest call; many
+        // rows take four accesses per lane, fewer barriers per byte.
+        if (wide) {
+            const int64_t nvec = p.dim / W;
+            if (nvec <= 1024 && (p.rows <= 2 * num_sms || nvec <= 32))
+                return norm_launch<T, P, W, 1>(p, st);
+            if (nvec <= 4096) return norm_launch<T, P, W, 4>(p, st);
+        } else {
+            if (p.dim <= 4096) return norm_launch<T, P, 1, 4>(p, st);
+            if (p.dim <= 16384) return norm_launch<T, P, 1, 16>(p, st);
+        }
+        const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
+        norm_any<T, P><<<blocks, NORM_THREADS, 0, st>>>(p);
         return cudaGetLastError();
+    };
+    return with_type(type, [&](auto t) {
+        return type == param_type ? typed(t, t) : typed(t, float{});
     });
 }
 
 size_t norm_grad_scratch(int64_t rows, int64_t dim, int num_sms) {
-    (void)num_sms;
-    return (size_t)slices_of(rows) * 2 * (size_t)dim * sizeof(float);
+    const int64_t slices = std::max(slices_any(rows), slices_rows(rows, 1, num_sms));
+    return (size_t)slices * 2 * (size_t)dim * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,
                                    const NormGradParams& p, int num_sms, cudaStream_t st) {
-    const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
-    const int slices = (int)slices_of(p.rows);
-    return with_type(type, [&](auto t) {
+    auto typed = [&](auto t, auto pt) {
         using T = decltype(t);
-        if (p.dweight || p.dbias) {
-            const dim3 grid((unsigned)((p.dim + 31) / 32), (unsigned)slices);
-            if (slices > 0) norm_dw_any<T><<<grid, 256, 0, st>>>(p);
-            const unsigned jb = (unsigned)((2 * p.dim + 255) / 256);
-            if (type == param_type) norm_dw_join<T><<<jb, 256, 0, st>>>(p, slices);
-            else norm_dw_join<float><<<jb, 256, 0, st>>>(p, slices);
-        }
-        // after the sums: dx may be dy
+        using P = decltype(pt);
+        constexpr int W = 16 / sizeof(T);
+        constexpr int K = 16 / W;                     // 16 elements of the row per lane
+        const bool sums = p.dweight || p.dbias;
+        int slices = 0;
+        cudaError_t e = cudaSuccess;
         if (p.rows > 0) {
-            if (type == param_type) norm_dx_any<T, T><<<blocks, NORM_THREADS, 0, st>>>(p);
-            else norm_dx_any<T, float><<<blocks, NORM_THREADS, 0, st>>>(p);
+            const bool wide = p.dim % W == 0 && rows_aligned16(p.x, p.ldx, sizeof(T)) &&
+                              rows_aligned16(p.dy, p.ld_dy, sizeof(T)) &&
+                              rows_aligned16(p.dx, p.ld_dx, sizeof(T)) &&
+                              (!p.weight || rows_aligned16(p.weight, 0, 1));
+            if (wide && p.dim <= NORM_GRAD_THREADS * 16) {
+                e = norm_grad_launch<T, P, W, K>(p, num_sms, st, &slices);
+            } else if (p.dim <= NORM_GRAD_THREADS * 4) {
+                e = norm_grad_launch<T, P, 1, 4>(p, num_sms, st, &slices);
+            } else if (p.dim <= NORM_GRAD_THREADS * 8) {
+                e = norm_grad_launch<T, P, 1, 8>(p, num_sms, st, &slices);
+            } else if (p.dim <= NORM_GRAD_THREADS * 16) {
+                e = norm_grad_launch<T, P, 1, 16>(p, num_sms, st, &slices);
+            } else {
+                // the sums first: dx may be dy
+                slices = (int)slices_any(p.rows);
+                if (sums) {
+                    const dim3 grid((unsigned)((p.dim + 31) / 32), (unsigned)slices);
+                    norm_dw_any<T><<<grid, 256, 0, st>>>(p);
+                }
+                const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
+                norm_dx_any<T, P><<<blocks, NORM_THREADS, 0, st>>>(p);
+                e = cudaGetLastError();
+            }
         }
-        return cudaGetLastError();
+        if (e != cudaSuccess || !sums) return e;
+        return launch_chained(norm_dw_join<P>, dim3((unsigned)((p.dim + 31) / 32), 2), dim3(256),
+                              0, st, p.rows > 0, p, slices);
+    };
+    return with_type(type, [&](auto t) {
+        return type == param_type ? typed(t, t) : typed(t, float{});
     });
 }
 
