@@ -80,58 +80,51 @@ cudaError_t launch_embed(const EmbedParams& p, int num_sms, cudaStream_t st) {
 
 // ---- gradient: sort ------------------------------------------------------------
 
-constexpr int SORT_TILE = 4096;      // keys sorted by one block in shared memory
-constexpr int SORT_THREADS = 1024;
+constexpr int SORT_TILE = 512;       // keys sorted by one block, one per thread
 constexpr int MERGE_WAYS = 16;       // sorted runs merged per round
 constexpr unsigned NO_ID = 0xffffffffu;
 
-// Sorts each tile of SORT_TILE tokens: a bitonic network on the 64-bit keys
-// in shared memory.  Ids outside [0, vocab) get the largest key and end up
-// behind every row.  Also zeroes the sums' arrival counters.  Pairs at distance <= 32 stay within one warp's 64 keys,
-// so those steps need no block barrier.
-__global__ __launch_bounds__(SORT_THREADS) void sort_tiles(const int* ids, int tokens,
-                                                           int64_t vocab, uint64_t* keys,
-                                                           int* arrived, int64_t counters) {
-    __shared__ uint64_t s[SORT_TILE];
+// Sorts each tile of SORT_TILE tokens with a bitonic network, one 64-bit key per
+// thread: exchanges within a warp are shuffles (35 of the 45 steps), the others
+// go through shared memory.  Small tiles, so that the SMs share the work: the
+// whole of 65,536 tokens takes 128 blocks.  Ids outside [0, vocab) get the
+// largest key and end up behind every row.  Also zeroes the sums' arrival counters.
+__global__ __launch_bounds__(SORT_TILE) void sort_tiles(const int* ids, int tokens, int64_t vocab,
+                                                        uint64_t* keys, int* arrived,
+                                                        int64_t counters) {
+    __shared__ uint64_t s[2][SORT_TILE];
     allow_successor();
-    for (int64_t i = (int64_t)blockIdx.x * SORT_THREADS + threadIdx.x; i < counters;
-         i += (int64_t)gridDim.x * SORT_THREADS)
-        arrived[i] = 0;
-    const int t0 = blockIdx.x * SORT_TILE;
-    const int n = min(SORT_TILE, tokens - t0);
-    int np = 64;
-    while (np < n) np <<= 1;
-    for (int i = threadIdx.x; i < np; i += SORT_THREADS) {
-        uint64_t key = ~0ull;
-        if (i < n) {
-            const int id = ids[t0 + i];
-            key = (uint64_t)(id >= 0 && id < vocab ? (unsigned)id : NO_ID) << 32 |
-                  (unsigned)(t0 + i);
-        }
-        s[i] = key;
+    const int t = threadIdx.x;
+    const int64_t at = (int64_t)blockIdx.x * SORT_TILE + t;
+    uint64_t key = ~0ull;
+    if (at < tokens) {
+        const int id = ids[at];
+        key = (uint64_t)(id >= 0 && id < vocab ? (unsigned)id : NO_ID) << 32 | (unsigned)at;
     }
-    bool wide = true;                // the last step crossed warps
-    for (int k = 2; k <= np; k <<= 1) {
+    for (int64_t i = at; i < counters; i += (int64_t)gridDim.x * SORT_TILE) arrived[i] = 0;
+    const int n = (int)min((int64_t)SORT_TILE, tokens - (int64_t)blockIdx.x * SORT_TILE);
+    int turn = 0;
+    // past the tile's keys there are only largest ones: a shorter network does
+    for (int k = 2; k < 2 * n; k <<= 1) {
         for (int j = k >> 1; j > 0; j >>= 1) {
-            if (wide || j > 32) __syncthreads();
-            else __syncwarp();
-            wide = j > 32;
-            for (int i = threadIdx.x; i < np / 2; i += SORT_THREADS) {
-                const int a = 2 * i - (i & (j - 1));
-                const int b = a + j;
-                const uint64_t x = s[a], y = s[b];
-                if ((x > y) == ((a & k) == 0)) {
-                    s[a] = y;
-                    s[b] = x;
-                }
+            uint64_t other;
+            if (j >= 32) {
+                // two buffers in turn: one barrier per exchange keeps them apart
+                s[turn][t] = key;
+                __syncthreads();
+                other = s[turn][t ^ j];
+                turn ^= 1;
+            } else {
+                other = __shfl_xor_sync(0xffffffffu, key, j);
             }
+            const bool up = (t & k) == 0, low = (t & j) == 0;
+            key = (up == low) == (key < other) ? key : other;
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += SORT_THREADS) keys[t0 + i] = s[i];
+    if (at < tokens) keys[at] = key;
 }
 
-// Number of keys below `key` in a[0..n), by halving steps of a fixed count.
+// Number of keys below `key` in a[0..n).
 __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t key) {
     int lo = 0, len = n;
     while (len > 0) {
@@ -146,8 +139,11 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
     return lo;
 }
 
-// Merges groups of MERGE_WAYS sorted runs of `run` keys: each key's place is
-// its own index plus the count of smaller keys in the other runs.
+// Merges groups of MERGE_WAYS sorted runs of `run` keys (a power of two): keys
+// are unique, so each key's place is the count of smaller keys over the group's
+// runs.  The searches of all runs take their steps together, MERGE_WAYS loads
+// at a time: a step costs one latency, not one for each run (65,536 keys:
+// 35 us per round with one search after the other).
 __global__ __launch_bounds__(256) void merge_runs(const uint64_t* in, uint64_t* out, int tokens,
                                                   int64_t run) {
     allow_successor();
@@ -155,14 +151,27 @@ __global__ __launch_bounds__(256) void merge_runs(const uint64_t* in, uint64_t* 
     const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (g >= tokens) return;
     const uint64_t key = in[g];
-    const int64_t own = g / run;
-    const int64_t first = own / MERGE_WAYS * MERGE_WAYS;
-    int64_t place = first * run + (g - own * run);
-    for (int64_t q = first; q < first + MERGE_WAYS; ++q) {
-        const int64_t start = q * run;
-        if (start >= tokens) break;
-        if (q != own)
-            place += count_below(in + start, (int)min(run, tokens - start), key);
+    const int64_t first = g / (run * MERGE_WAYS) * (run * MERGE_WAYS);
+    int64_t below[MERGE_WAYS];       // per run: start + keys known to be smaller
+#pragma unroll
+    for (int q = 0; q < MERGE_WAYS; ++q) below[q] = first + q * run;
+    for (int64_t half = run >> 1; half > 0; half >>= 1) {
+        uint64_t got[MERGE_WAYS];
+#pragma unroll
+        for (int q = 0; q < MERGE_WAYS; ++q) {
+            const int64_t at = below[q] + half - 1;
+            got[q] = at < tokens ? in[at] : ~0ull;
+        }
+#pragma unroll
+        for (int q = 0; q < MERGE_WAYS; ++q)
+            if (got[q] < key) below[q] += half;
+    }
+    // one candidate is left in each run
+    int64_t place = first;
+#pragma unroll
+    for (int q = 0; q < MERGE_WAYS; ++q) {
+        const int64_t at = below[q];
+        place += at - (first + q * run) + (at < tokens && in[at] < key);
     }
     out[place] = key;
 }
@@ -175,15 +184,17 @@ __global__ __launch_bounds__(256) void merge_runs(const uint64_t* in, uint64_t* 
 // run that crosses the piece's bounds leaves a partial sum, and the last of the
 // run's pieces to arrive adds the run's partials in piece order.
 constexpr int PANEL = 256;           // columns per warp: 512 bytes of a 16-bit row
-constexpr int PIECE_MIN = 8, PIECE_MAX = 256;
+constexpr int PIECE_MAX = 256;
+constexpr int64_t SUM_WARPS = 16384;
 
-// Tokens per piece: as many as leave about 16384 warps of work (three to four
-// times what the SMs hold at once), so that few runs are cut.  It depends on the
-// call's sizes only, so the order of every sum does too.
+// Tokens per piece: as many as leave about SUM_WARPS warps of work (three to four
+// times what the SMs hold at once), so that few runs are cut; one where there is
+// less, because a warp's tokens wait for one another.  It depends on the call's
+// sizes only, so the order of every sum does too.
 inline int64_t panels_of(int64_t dim) { return (dim + PANEL - 1) / PANEL; }
 inline int piece_of(int64_t tokens, int64_t dim) {
-    int piece = PIECE_MIN;
-    while (piece < PIECE_MAX && tokens * panels_of(dim) / piece > 16384) piece *= 2;
+    int piece = 1;
+    while (piece < PIECE_MAX && tokens * panels_of(dim) / piece > SUM_WARPS) piece *= 2;
     return piece;
 }
 inline int64_t padded(int64_t dim) { return (dim + 7) / 8 * 8; }   // partial rows: 32 bytes
@@ -360,13 +371,23 @@ template <typename G, int W>
 __device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t item, int lane) {
     const int64_t v0 = item * k.fill_rows;
     const int rows = (int)min((int64_t)k.fill_rows, p.vocab - v0);
-    bool absent = false;
-    if (lane < rows) {
-        const uint64_t key = (uint64_t)(v0 + lane) << 32;
-        const int at = count_below(k.keys, (int)p.tokens, key);
-        absent = at == p.tokens || k.keys[at] >> 32 != key >> 32;
+    const int n = (int)p.tokens;
+    const unsigned all = rows == 32 ? ~0u : (1u << rows) - 1;
+    // where the first of these rows would be, and 32 keys from there: enough unless
+    // its tokens are many, and then the other rows look for themselves
+    const int at = warp_count_below(k.keys, n, (uint64_t)v0 << 32, lane);
+    const uint64_t key = at + lane < n ? k.keys[at + lane] : ~0ull;
+    const int64_t row = (int64_t)(key >> 32) - v0;
+    unsigned present = __reduce_or_sync(0xffffffffu, row < rows ? 1u << row : 0u);
+    if (__shfl_sync(0xffffffffu, row, 31) < rows) {
+        bool here = false;
+        if (lane < rows) {
+            const int i = count_below(k.keys, n, (uint64_t)(v0 + lane) << 32);
+            here = i < n && (int64_t)(k.keys[i] >> 32) == v0 + lane;
+        }
+        present = __ballot_sync(0xffffffffu, here);
     }
-    const unsigned todo = __ballot_sync(0xffffffffu, absent);
+    const unsigned todo = all & ~present;
     for (int r = 0; r < rows; ++r) {
         if (!(todo >> r & 1)) continue;
         G* to = static_cast<G*>(p.dtable) + (v0 + r) * p.ld_dtable;
@@ -429,6 +450,17 @@ cudaError_t launch_embedding(spmm_type_t type, const EmbedParams& p, int num_sms
 
 size_t embed_grad_scratch(int64_t tokens, int64_t dim) { return grad_layout(tokens, dim).total; }
 
+// Pieces get longer as the work grows, so a smaller call may need more: what
+// covers every call.  pieces <= min(tokens, SUM_WARPS / panels + 1), or
+// tokens / PIECE_MAX + 1 once the pieces are longest; padded(dim) <= PANEL * panels.
+size_t embed_grad_scratch_upto(int64_t tokens, int64_t dim) {
+    const size_t wide = (size_t)padded(dim), most = (size_t)tokens / PIECE_MAX + 1;
+    const size_t rows = std::max(
+        std::min((size_t)tokens * wide, (size_t)SUM_WARPS * PANEL + wide), most * wide);
+    const size_t counters = std::max((size_t)SUM_WARPS + panels_of(dim), most * panels_of(dim));
+    return (size_t)tokens * 16 + counters * sizeof(int) + rows * 2 * sizeof(float) + 4 * 256;
+}
+
 cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
                                   const EmbedGradParams& p, char* scratch, int num_sms,
                                   cudaStream_t st) {
@@ -450,8 +482,8 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
         p.beta == 1.0f ? 0 : (p.vocab + k.fill_rows - 1) / k.fill_rows;
     if (p.tokens > 0) {
         const int tiles = (int)((p.tokens + SORT_TILE - 1) / SORT_TILE);
-        sort_tiles<<<tiles, SORT_THREADS, 0, st>>>(p.ids, (int)p.tokens, p.vocab, keys, k.arrived,
-                                                   k.sum_items);
+        sort_tiles<<<tiles, SORT_TILE, 0, st>>>(p.ids, (int)p.tokens, p.vocab, keys, k.arrived,
+                                                k.sum_items);
         cudaError_t e = cudaGetLastError();
         for (int64_t run = SORT_TILE; e == cudaSuccess && run < p.tokens; run *= MERGE_WAYS) {
             e = launch_chained(merge_runs, dim3((unsigned)((p.tokens + 255) / 256)), dim3(256), 0,

@@ -48,6 +48,7 @@ struct EmbedGradParams {
     float beta;
 };
 size_t embed_grad_scratch(int64_t tokens, int64_t dim);
+size_t embed_grad_scratch_upto(int64_t tokens, int64_t dim);   // of every call up to that
 cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
                                   const EmbedGradParams& p, char* scratch, int num_sms,
                                   cudaStream_t st);

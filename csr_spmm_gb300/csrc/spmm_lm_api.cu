@@ -41,8 +41,8 @@ spmm_status_t spmm_reserve_lm(spmm_handle_t h, int64_t rows, int64_t dim) {
     spmm_status_t s = lm_device(h, &sms);
     if (s != SPMM_OK) return s;
     char* base = nullptr;
-    return lm_scratch(h, std::max(embed_grad_scratch(rows, dim), norm_grad_scratch(rows, dim, sms)),
-                      &base);
+    return lm_scratch(h, std::max(embed_grad_scratch_upto(rows, dim),
+                                  norm_grad_scratch(rows, dim, sms)), &base);
 }
 
 spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale, const int32_t* ids,

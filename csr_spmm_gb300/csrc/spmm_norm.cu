@@ -319,10 +319,13 @@ __global__ __launch_bounds__(256) void norm_dw_any(NormGradParams p) {
 }
 
 // dweight and dbias from the slices' partial sums: a block takes 32 columns, each
-// of its warps every 8th slice in order, then the warps' sums are added in order.
+// of its warps every JOIN_WARPS-th slice in order, then the warps' sums are added
+// in order.  As many warps as a block may have: the sums are short, and what
+// counts is how many loads wait together.
+constexpr int JOIN_WARPS = 32;
 template <typename P>
-__global__ __launch_bounds__(256) void norm_dw_join(NormGradParams p, int slices) {
-    __shared__ float s[8][32];
+__global__ __launch_bounds__(32 * JOIN_WARPS) void norm_dw_join(NormGradParams p, int slices) {
+    __shared__ float s[JOIN_WARPS][32];
     wait_for_predecessor();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int which = blockIdx.y;
@@ -333,13 +336,13 @@ __global__ __launch_bounds__(256) void norm_dw_join(NormGradParams p, int slices
     if (c < p.dim) {
         const float* part = p.part + which * p.dim + c;
 #pragma unroll 8
-        for (int k = w; k < slices; k += 8) t += part[(int64_t)k * 2 * p.dim];
+        for (int k = w; k < slices; k += JOIN_WARPS) t += part[(int64_t)k * 2 * p.dim];
     }
     s[w][lane] = t;
     __syncthreads();
     if (w > 0 || c >= p.dim) return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += s[i][lane];
+    for (int i = 1; i < JOIN_WARPS; ++i) t += s[i][lane];
     out[c] = from_f32<P>(t);
 }
 
@@ -353,10 +356,11 @@ int warps_for(int64_t nvec, int K) {
 }
 
 // Slices of the register kernel's grid: one row at a time each, as many as the
-// SMs hold at NORM_GRAD_THREADS threads per SM.
-int64_t slices_rows(int64_t rows, int warps, int num_sms) {
-    return std::min<int64_t>(rows, (int64_t)num_sms * (NORM_GRAD_THREADS / 32) / warps);
+// SMs hold (`sm_warps` warps each, by the kernel's registers).
+int64_t slices_rows(int64_t rows, int warps, int num_sms, int sm_warps) {
+    return std::min<int64_t>(rows, (int64_t)num_sms * sm_warps / warps);
 }
+constexpr int SM_WARPS_MOST = 32;    // 64 registers a thread: up to 4 elements per lane
 
 template <typename T, typename P, int W, int K>
 cudaError_t norm_launch(const NormParams& p, cudaStream_t st) {
@@ -373,7 +377,8 @@ cudaError_t norm_grad_launch(const NormGradParams& p, int num_sms, cudaStream_t 
     const int nvec = (int)(p.dim / W);
     const int warps = warps_for(nvec, K);
     const int rows = std::max(1, 4 / warps);          // at least 128 threads
-    *slices = (int)slices_rows(p.rows, warps, num_sms);
+    constexpr int SM_WARPS = W * K <= 4 ? SM_WARPS_MOST : SM_WARPS_MOST / 2;
+    *slices = (int)slices_rows(p.rows, warps, num_sms, SM_WARPS);
     norm_grad_rows<T, P, W, K><<<(*slices + rows - 1) / rows, rows * warps * 32, 0, st>>>(
         p, warps, nvec, *slices);
     return cudaGetLastError();
@@ -413,7 +418,7 @@ cudaError_t launch_layer_norm(spmm_type_t type, spmm_type_t param_type, const No
 }
 
 size_t norm_grad_scratch(int64_t rows, int64_t dim, int num_sms) {
-    const int64_t slices = std::max(slices_any(rows), slices_rows(rows, 1, num_sms));
+    const int64_t slices = std::max(slices_any(rows), slices_rows(rows, 1, num_sms, SM_WARPS_MOST));
     return (size_t)slices * 2 * (size_t)dim * sizeof(float);
 }
 
@@ -453,8 +458,8 @@ cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,
             }
         }
         if (e != cudaSuccess || !sums) return e;
-        return launch_chained(norm_dw_join<P>, dim3((unsigned)((p.dim + 31) / 32), 2), dim3(256),
-                              0, st, p.rows > 0, p, slices);
+        return launch_chained(norm_dw_join<P>, dim3((unsigned)((p.dim + 31) / 32), 2),
+                              dim3(32 * JOIN_WARPS), 0, st, p.rows > 0, p, slices);
     };
     return with_type(type, [&](auto t) {
         return type == param_type ? typed(t, t) : typed(t, float{});

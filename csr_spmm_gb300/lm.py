@@ -17,6 +17,10 @@ from . import _lib
 
 _TYPES = {torch.float32: _lib.SPMM_F32, torch.float16: _lib.SPMM_F16,
           torch.bfloat16: _lib.SPMM_BF16}
+_F32, _I32 = torch.float32, torch.int32
+
+# Small calls are bound by this file (a kernel of 2 us behind 10 us of Python), so
+# each check reads a tensor's attributes once and nothing is built on the way.
 
 
 def _type(t, what: str) -> int:
@@ -28,76 +32,68 @@ def _type(t, what: str) -> int:
 
 def _matrix(t, what: str):
     """(rows, columns, leading dimension) of a matrix."""
-    if t.dim() != 2:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
         raise ValueError(f"{what} must be 2-D with unit column stride")
-    rows, cols = t.shape
-    if cols > 1 and rows > 0 and t.stride(1) != 1:
+    rows, cols = shape
+    if stride[1] != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{what} must be 2-D with unit column stride")
-    return rows, cols, (t.stride(0) if rows > 1 else max(1, cols))
+    return rows, cols, (stride[0] if rows > 1 else cols or 1)
 
 
 def _vector(t, n: int, dtype, what: str) -> None:
-    """A 1-D array of n contiguous entries of one of the types in `dtype`."""
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{what} must be 1-D with {n} entries, got {tuple(t.shape)}")
-    if t.dtype not in dtype:
-        raise TypeError(f"{what} must be {' or '.join(str(d)[6:] for d in dtype)}")
+    """A 1-D array of n contiguous entries of one type."""
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != n:
+        raise ValueError(f"{what} must be 1-D with {n} entries, got {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {str(dtype)[6:]}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{what} must be contiguous")
-
-
-_INT, _FLOAT = (torch.int32,), (torch.float32,)
 
 
 def _address(t, device: int) -> int:
     """Device address of a tensor on the handle's GPU (0 for None)."""
     if t is None:
         return 0
-    if not t.is_cuda:
-        raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
-    if t.device.index != device:
+    if t.get_device() != device:
+        if not t.is_cuda:
+            raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
         raise ValueError(f"tensor on {t.device}, but the handle is on cuda:{device}")
     return t.data_ptr()
 
 
-class _Call:
-    """The stream of one call: where its outputs are allocated and what it holds."""
-
-    def __init__(self, handle, stream, tensors):
-        self.device = handle.device
-        self.given = stream
-        self.addresses = [_address(t, self.device) for t in tensors]
-        if stream is None:
-            self.stream = torch.cuda.current_stream().cuda_stream
-        else:
-            self.stream = stream.cuda_stream
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-
-    def empty(self, shape, dtype):
-        if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.given):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+def _current(device: int) -> int:
+    """Torch's current stream on the handle's GPU."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _output(call, out, rows: int, cols: int, dtype):
-    """A [rows, cols] output: `out` after its checks, or a new tensor."""
-    if out is None:
-        out = call.empty((rows, cols), dtype)
-        return out, out.data_ptr(), max(1, cols)
-    return out, _address(out, call.device), _matrix(out, "out")[2]
+def _new(shape, dtype, device: int, stream):
+    """A tensor for an output, allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _check_out(out, rows: int, cols: int, dtype) -> None:
-    if out is None:
-        return
-    if tuple(out.shape) != (rows, cols):
-        raise ValueError(f"out must be {(rows, cols)}, got {tuple(out.shape)}")
-    _matrix(out, "out")
+def _enter(device: int, stream, tensors) -> int:
+    """The call's stream; on a given one the tensors' memory is held until it is used."""
+    if stream is None:
+        return _current(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _check_out(out, rows: int, cols: int, dtype) -> int:
+    """Leading dimension of a given [rows, cols] output."""
+    shape = out.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"out must be {(rows, cols)}, got {tuple(shape)}")
     if out.dtype != dtype:
         raise TypeError(f"out must be {str(dtype)[6:]}")
+    return _matrix(out, "out")[2]
 
 
 def embedding(handle, ids, table, scale: float = 1.0, out=None, stream=None):
@@ -109,13 +105,17 @@ def embedding(handle, ids, table, scale: float = 1.0, out=None, stream=None):
     code = _type(table, "table")
     vocab, dim, ld = _matrix(table, "table")
     n = ids.numel()
-    _vector(ids, n, _INT, "ids")
-    _check_out(out, n, dim, table.dtype)
-    call = _Call(handle, stream, (ids, table, out))
-    a_ids, a_table, _ = call.addresses
-    out, a_out, ld_out = _output(call, out, n, dim, table.dtype)
-    _lib.spmm_embedding(handle.ptr, code, scale, a_ids, n, a_table, ld, vocab, dim, a_out, ld_out,
-                        call.stream)
+    _vector(ids, n, _I32, "ids")
+    ld_out = dim or 1
+    if out is not None:
+        ld_out = _check_out(out, n, dim, table.dtype)
+    device = handle.device
+    a_ids, a_table = _address(ids, device), _address(table, device)
+    st = _enter(device, stream, (ids, table, out))
+    if out is None:
+        out = _new((n, dim), table.dtype, device, stream)
+    _lib.spmm_embedding(handle.ptr, code, scale, a_ids, n, a_table, ld, vocab, dim,
+                        _address(out, device), ld_out, st)
     return out
 
 
@@ -134,24 +134,28 @@ def embedding_grad(handle, ids, dout, dtable, scale: float = 1.0, beta: float = 
     vocab, cols, ld_table = _matrix(dtable, "dtable")
     if cols != dim:
         raise ValueError(f"shape mismatch: dout {tuple(dout.shape)}, dtable {tuple(dtable.shape)}")
-    _vector(ids, n, _INT, "ids")
-    call = _Call(handle, stream, (ids, dout, dtable))
-    a_ids, a_dout, a_table = call.addresses
+    _vector(ids, n, _I32, "ids")
+    device = handle.device
+    a_ids, a_dout, a_table = (_address(ids, device), _address(dout, device),
+                              _address(dtable, device))
     _lib.spmm_embedding_grad(handle.ptr, code, grad_code, scale, a_ids, n, a_dout, ld, beta,
-                             a_table, ld_table, vocab, dim, call.stream)
+                             a_table, ld_table, vocab, dim,
+                             _enter(device, stream, (ids, dout, dtable)))
 
 
-def _params(x, dim: int, weight, bias) -> int:
+def _params(x, code: int, dim: int, weight, bias) -> int:
     """The type code shared by weight and bias: x's or float32."""
     given = weight if weight is not None else bias
     if given is None:
-        return _TYPES[x.dtype]
-    if given.dtype != x.dtype and given.dtype != torch.float32:
+        return code
+    dtype = given.dtype
+    if dtype != x.dtype and dtype != _F32:
         raise TypeError("weight and bias must have x's dtype or be float32")
-    for t, what in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _vector(t, dim, (given.dtype,), what)
-    return _TYPES[given.dtype]
+    if weight is not None:
+        _vector(weight, dim, dtype, "weight")
+    if bias is not None:
+        _vector(bias, dim, dtype, "bias")
+    return _TYPES[dtype]
 
 
 def layer_norm(handle, x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
@@ -163,17 +167,19 @@ def layer_norm(handle, x, weight=None, bias=None, eps: float = 1e-5, out=None, s
     """
     code = _type(x, "x")
     rows, dim, ld = _matrix(x, "x")
-    param_code = _params(x, dim, weight, bias)
-    _check_out(out, rows, dim, x.dtype)
-    call = _Call(handle, stream, (x, weight, bias, out))
-    a_x, a_w, a_b, _ = call.addresses
-    y, a_y, ld_y = _output(call, out, rows, dim, x.dtype)
-    stats = call.empty((2, rows), torch.float32)
-    mean, rstd = stats[0], stats[1]
-    a_stats = stats.data_ptr()
-    _lib.spmm_layer_norm(handle.ptr, code, param_code, a_x, ld, rows, dim, a_w, a_b, eps, a_y,
-                         ld_y, a_stats, a_stats + 4 * rows, call.stream)
-    return y, mean, rstd
+    param_code = _params(x, code, dim, weight, bias)
+    ld_y = dim or 1
+    if out is not None:
+        ld_y = _check_out(out, rows, dim, x.dtype)
+    device = handle.device
+    a_x, a_w, a_b = _address(x, device), _address(weight, device), _address(bias, device)
+    st = _enter(device, stream, (x, weight, bias, out))
+    if out is None:
+        out = _new((rows, dim), x.dtype, device, stream)
+    mean, rstd = _new(rows, _F32, device, stream), _new(rows, _F32, device, stream)
+    _lib.spmm_layer_norm(handle.ptr, code, param_code, a_x, ld, rows, dim, a_w, a_b, eps,
+                         _address(out, device), ld_y, mean.data_ptr(), rstd.data_ptr(), st)
+    return out, mean, rstd
 
 
 def layer_norm_grad(handle, dy, x, mean, rstd, weight=None, bias: bool = True, out=None,
@@ -186,26 +192,35 @@ def layer_norm_grad(handle, dy, x, mean, rstd, weight=None, bias: bool = True, o
     """
     code = _type(x, "x")
     rows, dim, ld = _matrix(x, "x")
-    if tuple(dy.shape) != (rows, dim):
+    dy_rows, dy_dim, ld_dy = _matrix(dy, "dy")
+    if dy_rows != rows or dy_dim != dim:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, dy {tuple(dy.shape)}")
     if dy.dtype != x.dtype:
         raise TypeError("x and dy must share one dtype")
-    ld_dy = _matrix(dy, "dy")[2]
-    _vector(mean, rows, _FLOAT, "mean")
-    _vector(rstd, rows, _FLOAT, "rstd")
-    param_code = _params(x, dim, weight, None)
-    _check_out(out, rows, dim, x.dtype)
-    call = _Call(handle, stream, (dy, x, mean, rstd, weight, out))
-    a_dy, a_x, a_mean, a_rstd, a_w, _ = call.addresses
-    dx, a_dx, ld_dx = _output(call, out, rows, dim, x.dtype)
+    _vector(mean, rows, _F32, "mean")
+    _vector(rstd, rows, _F32, "rstd")
+    param_code = _params(x, code, dim, weight, None)
+    ld_dx = dim or 1
+    if out is not None:
+        ld_dx = _check_out(out, rows, dim, x.dtype)
+    device = handle.device
+    a_dy, a_x, a_w = _address(dy, device), _address(x, device), _address(weight, device)
+    a_mean, a_rstd = _address(mean, device), _address(rstd, device)
+    st = _enter(device, stream, (dy, x, mean, rstd, weight, out))
+    if out is None:
+        out = _new((rows, dim), x.dtype, device, stream)
     pt = x.dtype if weight is None else weight.dtype
-    dweight = call.empty(dim, pt) if weight is not None else None
-    dbias = call.empty(dim, pt) if bias else None
+    dweight = dbias = None
+    a_dw = a_db = 0
+    if weight is not None:
+        dweight = _new(dim, pt, device, stream)
+        a_dw = dweight.data_ptr()
+    if bias:
+        dbias = _new(dim, pt, device, stream)
+        a_db = dbias.data_ptr()
     _lib.spmm_layer_norm_grad(handle.ptr, code, param_code, a_dy, ld_dy, a_x, ld, a_mean, a_rstd,
-                              a_w, rows, dim, a_dx, ld_dx,
-                              0 if dweight is None else dweight.data_ptr(),
-                              0 if dbias is None else dbias.data_ptr(), call.stream)
-    return dx, dweight, dbias
+                              a_w, rows, dim, _address(out, device), ld_dx, a_dw, a_db, st)
+    return out, dweight, dbias
 
 
 def token_logprob(handle, logits, targets=None, alpha: float = 1.0, top: int = 0, stream=None):
@@ -219,25 +234,24 @@ def token_logprob(handle, logits, targets=None, alpha: float = 1.0, top: int = 0
     code = _type(logits, "logits")
     rows, vocab, ld = _matrix(logits, "logits")
     if targets is not None:
-        _vector(targets, rows, _INT, "targets")
+        _vector(targets, rows, _I32, "targets")
     if not 0 <= top <= _lib.SPMM_TOP_MAX:
         raise ValueError(f"top must be between 0 and {_lib.SPMM_TOP_MAX}")
-    call = _Call(handle, stream, (logits, targets))
-    a_x, a_t = call.addresses
-    # one allocation for the vectors, the first a row without a target leaves out
-    out = call.empty((3, rows), torch.float32)
-    logprob, entropy, lse = out[0], out[1], out[2]
-    a_out = out.data_ptr()
-    top_logprob = top_index = None
+    device = handle.device
+    a_x, a_t = _address(logits, device), _address(targets, device)
+    st = _enter(device, stream, (logits, targets))
+    entropy, lse = _new(rows, _F32, device, stream), _new(rows, _F32, device, stream)
+    logprob = top_logprob = top_index = None
+    a_lp = a_tl = a_ti = 0
+    if targets is not None:
+        logprob = _new(rows, _F32, device, stream)
+        a_lp = logprob.data_ptr()
     if top:
-        top_logprob = call.empty((rows, top), torch.float32)
-        top_index = call.empty((rows, top), torch.int32)
-    _lib.spmm_token_logprob(handle.ptr, code, alpha, a_x, ld, rows, vocab, a_t, top,
-                            a_out if targets is not None else 0, a_out + 4 * rows,
-                            a_out + 8 * rows, top_logprob.data_ptr() if top else 0,
-                            top_index.data_ptr() if top else 0, call.stream)
-    if targets is None:
-        logprob = None
+        top_logprob = _new((rows, top), _F32, device, stream)
+        top_index = _new((rows, top), _I32, device, stream)
+        a_tl, a_ti = top_logprob.data_ptr(), top_index.data_ptr()
+    _lib.spmm_token_logprob(handle.ptr, code, alpha, a_x, ld, rows, vocab, a_t, top, a_lp,
+                            entropy.data_ptr(), lse.data_ptr(), a_tl, a_ti, st)
     return (logprob, entropy, lse, top_logprob, top_index) if top else (logprob, entropy, lse)
 
 
@@ -252,24 +266,31 @@ def token_logprob_grad(handle, logits, targets, lse, entropy=None, dlogprob=None
     """
     code = _type(logits, "logits")
     rows, vocab, ld = _matrix(logits, "logits")
-    if dlogprob is not None and targets is None:
-        raise ValueError("dlogprob needs the targets")
-    if dentropy is not None and entropy is None:
-        raise ValueError("dentropy needs the entropy")
     if dlogprob is None:
         targets = None
+    elif targets is None:
+        raise ValueError("dlogprob needs the targets")
+    else:
+        _vector(targets, rows, _I32, "targets")
+        _vector(dlogprob, rows, _F32, "dlogprob")
     if dentropy is None:
         entropy = None
-    if targets is not None:
-        _vector(targets, rows, _INT, "targets")
-    for t, what in ((lse, "lse"), (entropy, "entropy"), (dlogprob, "dlogprob"),
-                    (dentropy, "dentropy")):
-        if t is not None:
-            _vector(t, rows, _FLOAT, what)
-    _check_out(out, rows, vocab, logits.dtype)
-    call = _Call(handle, stream, (logits, targets, lse, entropy, dlogprob, dentropy, out))
-    a_x, a_t, a_lse, a_ent, a_dl, a_de, _ = call.addresses
-    out, a_out, ld_out = _output(call, out, rows, vocab, logits.dtype)
+    elif entropy is None:
+        raise ValueError("dentropy needs the entropy")
+    else:
+        _vector(entropy, rows, _F32, "entropy")
+        _vector(dentropy, rows, _F32, "dentropy")
+    _vector(lse, rows, _F32, "lse")
+    ld_out = vocab or 1
+    if out is not None:
+        ld_out = _check_out(out, rows, vocab, logits.dtype)
+    device = handle.device
+    a_x, a_t, a_lse = _address(logits, device), _address(targets, device), _address(lse, device)
+    a_ent, a_dl, a_de = (_address(entropy, device), _address(dlogprob, device),
+                         _address(dentropy, device))
+    st = _enter(device, stream, (logits, targets, lse, entropy, dlogprob, dentropy, out))
+    if out is None:
+        out = _new((rows, vocab), logits.dtype, device, stream)
     _lib.spmm_token_logprob_grad(handle.ptr, code, alpha, a_x, ld, rows, vocab, a_t, a_lse, a_ent,
-                                 a_dl, a_de, a_out, ld_out, call.stream)
+                                 a_dl, a_de, _address(out, device), ld_out, st)
     return out

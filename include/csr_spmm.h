@@ -486,8 +486,9 @@ spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale,
  * type `type`, dtable `grad_type`, which is `type` or SPMM_F32.  The tokens are
  * sorted by id on the device (stable), and each row's sum is taken in binary32
  * over pieces of consecutive sorted tokens whose bounds depend on `tokens`
- * alone, then over the pieces in order.  Scratch: 16 bytes per token and at
- * most 1/4 of the bytes of dout in binary32.  tokens <= 2^30. */
+ * and `dim` alone, then over the pieces in order.  Scratch: 16 bytes per token,
+ * and for the rows that pieces share 8 bytes per element of dout or, where that
+ * is less, about 34 MB or 1/32 byte per element, the larger.  tokens <= 2^30. */
 spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t grad_type,
                                   float scale, const int32_t *ids, int64_t tokens,
                                   const void *dout, int64_t ld_dout, float beta,
@@ -515,7 +516,8 @@ spmm_status_t spmm_layer_norm(spmm_handle_t h, spmm_type_t type, spmm_type_t par
  * dx has type `type` and may be dy; dweight and dbias have type `param_type`
  * (either may be NULL: not computed) and are overwritten (zeros for
  * rows == 0).  weight NULL means 1.  mean and rstd as spmm_layer_norm wrote
- * them.  Scratch: at most 64 KB * dim, no more than 8 * rows * dim bytes. */
+ * them.  Scratch: 8 bytes per column for each slice of the rows, of which there
+ * are at most 32 per SM or rows / 256, the larger, and no more than rows. */
 spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t param_type,
                                    const void *dy, int64_t ld_dy, const void *x, int64_t ldx,
                                    const float *mean, const float *rstd, const void *weight,

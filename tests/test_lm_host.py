@@ -112,6 +112,9 @@ class _AsCuda(torch.Tensor):
     def device(self):
         return torch.device("cuda", 0)
 
+    def get_device(self):
+        return 0
+
 
 def _cuda(t):
     return torch.Tensor._make_subclass(_AsCuda, t)
@@ -122,8 +125,7 @@ def test_calls_pass_addresses_and_leading_dimensions(monkeypatch):
     for name in ("spmm_embedding", "spmm_embedding_grad", "spmm_layer_norm",
                  "spmm_layer_norm_grad", "spmm_token_logprob", "spmm_token_logprob_grad"):
         monkeypatch.setattr(_lib, name, lambda *a, name=name: calls.append((name, a)))
-    monkeypatch.setattr(torch.cuda, "current_stream",
-                        lambda *a: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(cs.lm, "_current", lambda device: 77)
     h = types.SimpleNamespace(ptr=1234, device=0)
     ids, table, out = _cuda(IDS.clone()), _cuda(F(5, 10))[:, :8], _cuda(F(3, 12))[:, :8]
     assert cs.embedding(h, ids, table, scale=2.0, out=out) is out
