@@ -27,7 +27,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 // W consecutive elements as they lie in memory: W > 1 in 32-bit words, so that
 // 16-bit elements stay packed in registers until they are used.
 template <typename T, int W>
-struct Vec {
+struct alignas(sizeof(T) * W % 16 == 0 ? 16 : 4) Vec {
     static constexpr int WORDS = (int)sizeof(T) * W / 4;
     uint32_t w[WORDS];
 };
@@ -116,6 +116,54 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[W]) {
         if (C == Cache::STREAM) __stcs(p, v);
         else *p = v;
     }
+}
+
+// Asynchronous copies of a Vec into the issuing thread's own slot of shared
+// memory: no registers wait for them, and since no other thread reads the slot,
+// no barrier is needed either.  4 or 16 bytes (single 16-bit elements have none).
+template <typename T, int W>
+constexpr bool can_copy_async = sizeof(T) * W >= 4;
+template <typename T, int W>
+__device__ __forceinline__ void copy_async(Vec<T, W>* to, const T* from) {
+    const unsigned a = (unsigned)__cvta_generic_to_shared(to);
+    if constexpr (sizeof(T) * W == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(a), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_issued() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most N later groups of copies are outstanding.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two binary32 operations in one instruction (sm_100 and later); each half is
+// rounded as the single operation would be.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void halves(uint64_t r, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {

@@ -101,221 +101,279 @@ struct Row {
     }
 };
 
-// Largest of an access's elements, NaNs left out.
-template <typename T, int W>
-__device__ __forceinline__ float vec_max(const Vec<T, W>& v) {
-    if constexpr (sizeof(T) == 4) {
-        return fmaxf(fmaxf(__uint_as_float(v.w[0]), __uint_as_float(v.w[1])),
-                     fmaxf(__uint_as_float(v.w[2]), __uint_as_float(v.w[3])));
-    } else if constexpr (std::is_same_v<T, __half>) {
-        const __half2* h = reinterpret_cast<const __half2*>(v.w);
-        const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-        return fmaxf(__low2float(m), __high2float(m));
-    } else {
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(v.w);
-        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-        return fmaxf(__low2float(m), __high2float(m));
+// Largest elements of accesses, NaNs left out, packed as the elements are; and
+// the accesses' elements kept from falling below `low` (NaN stays NaN).
+template <typename T>
+struct Largest {
+    using Pair = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+    Pair m, low;
+
+    __device__ explicit Largest(float least) : m(both(-INFINITY)), low(both(least)) {}
+    __device__ static Pair both(float x) {
+        if constexpr (std::is_same_v<T, __half>) return __float2half2_rn(x);
+        else return __float2bfloat162_rn(x);
     }
-}
+    __device__ void see(const Vec<T, 8>& v) {
+        const Pair* x = reinterpret_cast<const Pair*>(v.w);
+        m = __hmax2(m, __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3])));
+    }
+    __device__ float value() const { return fmaxf(__low2float(m), __high2float(m)); }
+    __device__ void floor(const Vec<T, 8>& v, float (&f)[8]) const {
+        Vec<T, 8> r;
+        const Pair* x = reinterpret_cast<const Pair*>(v.w);
+        Pair* y = reinterpret_cast<Pair*>(r.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __hmax2_nan(x[i], low);
+        unpack(r, f);
+    }
+};
+template <>
+struct Largest<float> {
+    float m, low;
+
+    __device__ explicit Largest(float least) : m(-INFINITY), low(least) {}
+    __device__ void see(const Vec<float, 4>& v) {
+        float f[4];
+        unpack(v, f);
+        m = fmaxf(m, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+    }
+    __device__ float value() const { return m; }
+    __device__ void floor(const Vec<float, 4>& v, float (&f)[4]) const {
+        unpack(v, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = max_nan(f[i], low);
+    }
+};
 
 // ---- forward --------------------------------------------------------------------------
 
 constexpr int LP_WARPS = 8;                     // at most
 constexpr int UNITS = 4;                        // accesses in flight per lane
-constexpr int GROUPS = 32 * LP_WARPS;           // groups of the selection, at most
 constexpr int CANDIDATES = SPMM_TOP_MAX * SPMM_TOP_MAX;
 
-// Sums of a part of a row.  The base is c * max(m, -lim), rounded: every use must see
+// Sums of a part of a row.  The base is c * max(m, low), rounded: every use must see
 // the same number, so the product may not become part of a fused multiply-add.
 struct Sums {
     float m, s, u;
 };
-__device__ __forceinline__ float base_of(float m, float c, float lim) {
-    return __fmul_rn(fmaxf(m, -lim), c);
+__device__ __forceinline__ float base_of(float m, float c, float low) {
+    return __fmul_rn(fmaxf(m, low), c);
 }
-__device__ __forceinline__ void add(Sums& a, const Sums& b, float c, float lim) {
+// A part's sums from its own base to the one `d` above it (d <= 0).
+__device__ __forceinline__ void rebase(float& s, float& u, float d) {
+    const float e = exp2_approx(d);
+    u = e * fmaf(fmaxf(d, -200.0f), s, u);      // no weight is left long before -200
+    s *= e;
+}
+__device__ __forceinline__ void add(Sums& a, Sums b, float c, float low) {
     const float m = fmaxf(a.m, b.m);
-    const float base = base_of(m, c, lim);
-    const float da = base_of(a.m, c, lim) - base, db = base_of(b.m, c, lim) - base;
-    const float ea = exp2_approx(da), eb = exp2_approx(db);
-    // a part without weight (e == 0) may be any distance away
-    a.u = ea * (a.u + (ea > 0.0f ? da : 0.0f) * a.s) + eb * (b.u + (eb > 0.0f ? db : 0.0f) * b.s);
-    a.s = ea * a.s + eb * b.s;
+    const float base = base_of(m, c, low);
+    rebase(a.s, a.u, base_of(a.m, c, low) - base);
+    rebase(b.s, b.u, base_of(b.m, c, low) - base);
     a.m = m;
+    a.s += b.s;
+    a.u += b.u;
 }
 
 struct RowShared {
     Sums sums[LP_WARPS];
     Sums total;                                 // this block's part of the row
     uint64_t best[SPMM_TOP_MAX];                // its alternatives, largest first (0: none)
-    unsigned group_max[GROUPS];                 // order_of each group's largest logit
-    int chosen[SPMM_TOP_MAX];                   // the groups that hold the alternatives
+    unsigned chosen[32 * LP_WARPS];             // lanes whose logits hold the alternatives
     int chosen_count;
     int count;
     uint64_t list[CANDIDATES];
 };
 
+// How a block's threads share its part of a row: units of 32 accesses, each warp
+// UNITS at a time.  Thread t takes the accesses j0 + i * 32 + lane of its turns.
+struct Part {
+    int64_t unit0, units;
+    int warps;
+    __device__ int64_t turns() const { return (units + (int64_t)warps * UNITS - 1) / (warps * UNITS); }
+    // the q-th access of thread t (one past the end of its part: -1)
+    __device__ int64_t access(int t, int64_t q) const {
+        const int64_t unit = (q / UNITS * warps + t / 32) * UNITS + q % UNITS;
+        return unit < units ? (unit0 + unit) * 32 + t % 32 : -1;
+    }
+};
+
+// Adds an access's elements of order >= least to the list of candidates.
+template <typename T>
+__device__ __forceinline__ void collect(RowShared& sh, const Row<T>& row, int64_t j, unsigned least) {
+    constexpr int W = Row<T>::W;
+    float f[W];
+    unpack(row.template load<Cache::KEEP>(j), f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const unsigned order = order_of(f[i]);
+        if (order < least) continue;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < CANDIDATES) sh.list[at] = rank_key(order, (unsigned)(j * W + i - row.off));
+    }
+}
+
 // The alternatives of this block's part of the row, into sh.best.
 //
-// The part's accesses fall into groups of 2^shift, contiguous and in index order,
-// at most one group per thread.  Take the k groups whose largest logits rank highest (equal
-// ones by lowest group): every alternative lies in one of them, since an
-// element of another group is beaten by the largest of each of the k.  The
-// smallest of the k maxima, tau, is a lower bound of the alternatives' values.
-// So a second look at k groups (in L2) is enough: collect what lies above tau,
-// and of each group's elements equal to tau the first k, then rank that short
-// list.  Only a row with more than CANDIDATES such elements takes k rounds of
-// the largest one left.
+// `mine` is the order of the largest of this thread's logits.  tau, the k-th largest
+// of the threads' values, is a lower bound of the k-th largest logit, and every
+// logit that reaches it belongs to a thread whose own largest does.  So a second look
+// (in L2) at the logits of those threads, k of them unless some are equal, gives a
+// short list that holds the alternatives; its entries are ranked by counting.
+// When more than CANDIDATES logits reach tau, nearly all must equal it: the list is
+// then made of those above tau, and the first equal ones in index order.
 template <typename T>
-__device__ void choose(RowShared& sh, const Row<T>& row, int64_t unit0, int64_t units, int shift,
-                       int k) {
+__device__ void choose(RowShared& sh, const Row<T>& row, const Part& part, unsigned mine, int k) {
     constexpr int W = Row<T>::W;
-    const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
-    const unsigned mine = sh.group_max[tid];
-    // tau: the largest order that at least k groups reach (0: fewer than k have any)
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    // the largest number that the values of at least k threads reach, bit by bit (a
+    // 16-bit logit has only the upper bits; 0: fewer than k have any)
     unsigned tau = 0;
-    for (int bit = 31; bit >= 0; --bit) {
+    constexpr int LOW = sizeof(T) == 4 ? 0 : std::is_same_v<T, __half> ? 13 : 16;
+    for (int bit = 31; bit >= LOW; --bit) {
         const unsigned next = tau | 1u << bit;
         if (__syncthreads_count(mine >= next) >= k) tau = next;
     }
+    // of negative logits the lower bits are all set
+    if (LOW > 0 && tau > 0 && tau < 0x80000000u) tau |= (1u << LOW) - 1;
     if (tid < k) sh.best[tid] = 0;
-    if (tid == 0) {
-        sh.chosen_count = 0;
-        sh.count = 0;
-    }
+    if (tid == 0) sh.chosen_count = sh.count = 0;
     __syncthreads();
-    // groups above tau, then those equal to tau from the lowest; for tau == 0 all that have any
-    if (mine > tau) sh.chosen[atomicAdd(&sh.chosen_count, 1)] = tid;
-    __syncthreads();
-    if (tau > 0 && tid < 32) {
-        int have = sh.chosen_count;
-        for (int g = lane; have < k && g - lane < (int)blockDim.x; g += 32) {
-            const unsigned equal = __ballot_sync(ALL, sh.group_max[g] == tau);
-            const int at = have + __popc(equal & ((1u << lane) - 1));
-            if ((equal >> lane & 1) && at < k) sh.chosen[at] = g;
-            have += __popc(equal);
-        }
-        if (lane == 0) sh.chosen_count = min(have, k);
-    }
+    const unsigned least = max(tau, 1u);
+    if (mine >= least) sh.chosen[atomicAdd(&sh.chosen_count, 1)] = tid;
     __syncthreads();
     const int chosen = sh.chosen_count;
-    const unsigned least = max(tau, 1u);
-    // 32 lanes, or 2^shift where that is less, per group; its elements in index order
-    const int width = min(32, 1 << shift), together = 32 / width;
-    const int64_t j_end = (unit0 + units) * 32;
-    const int steps = shift > 5 ? 1 << (shift - 5) : 1;
-    for (int q0 = (tid >> 5) * together; q0 < chosen; q0 += warps * together) {
-        const int q = q0 + lane / width;
-        int64_t j = unit0 * 32 + (lane & (width - 1));
-        j = q < chosen ? j + ((int64_t)sh.chosen[q] << shift) : j_end;
-        int equal_seen = 0;
-        for (int step = 0; step < steps; ++step, j += 32) {
-            unsigned order[W];
-            int equal = 0;
-            bool any = false;
-            if (j < j_end) {
+    const int64_t own = part.turns() * UNITS;       // accesses of a thread, at most
+    for (int g = w; g < chosen; g += part.warps)
+        for (int64_t q = lane; q < own; q += 32) {
+            const int64_t j = part.access(sh.chosen[g], q);
+            if (j >= 0) collect(sh, row, j, least);
+        }
+    __syncthreads();
+    if (sh.count > CANDIDATES) {
+        __syncthreads();
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        for (int g = w; g < chosen; g += part.warps)
+            for (int64_t q = lane; q < own; q += 32) {
+                const int64_t j = part.access(sh.chosen[g], q);
+                if (j >= 0) collect(sh, row, j, least + 1);
+            }
+        __syncthreads();
+        const int above = sh.count;
+        __syncthreads();
+        if (above > CANDIDATES) {
+            // many far above the others, all in a few threads' hands: k rounds of the
+            // largest one left
+            uint64_t last = ~0ull;
+            for (int round = 0; round < k; ++round) {
+                uint64_t best = 0;
+                for (int g = w; g < chosen; g += part.warps)
+                    for (int64_t q = lane; q < own; q += 32) {
+                        const int64_t j = part.access(sh.chosen[g], q);
+                        if (j < 0) continue;
+                        float f[W];
+                        unpack(row.template load<Cache::KEEP>(j), f);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            const unsigned order = order_of(f[i]);
+                            const uint64_t key =
+                                rank_key(order, (unsigned)(j * W + i - row.off));
+                            if (order > 0 && key < last && key > best) best = key;
+                        }
+                    }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(ALL, best, o));
+                if (lane == 0) sh.list[w] = best;
+                __syncthreads();
+                for (int i = 0; i < part.warps; ++i) best = max(best, sh.list[i]);
+                __syncthreads();
+                last = best;
+                if (tid == 0) sh.best[round] = best;
+            }
+            __syncthreads();
+            return;
+        }
+        if (w == 0 && tau > 0) {
+            // the equal ones, in index order until there are enough
+            int have = above;
+            for (int64_t u = 0; u < part.units && have < k; ++u) {
+                const int64_t j = (part.unit0 + u) * 32 + lane;
                 float f[W];
                 unpack(row.template load<Cache::KEEP>(j), f);
+                int equal = 0;
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    order[i] = order_of(f[i]);
-                    any |= order[i] >= least;
-                    equal += order[i] == least;
+                for (int i = 0; i < W; ++i) equal += order_of(f[i]) == tau;
+                int at = equal;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(ALL, at, o);
+                    if (lane >= o) at += up;
                 }
-            }
-            if (!__any_sync(ALL, any)) continue;
-            int before = equal;                 // equal ones in the group's lower lanes
-            for (int o = 1; o < width; o <<= 1) {
-                const int up = __shfl_up_sync(ALL, before, o, width);
-                if ((lane & (width - 1)) >= o) before += up;
-            }
-            const int all = __shfl_sync(ALL, before, width - 1, width);
-            before += equal_seen - equal;
-            equal_seen += all;
-            if (!any) continue;
+                const int all = __shfl_sync(ALL, at, 31);
+                at += have - equal;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                if (order[i] < least) continue;
-                if (order[i] == least && before++ >= k) continue;
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < CANDIDATES)
-                    sh.list[at] = rank_key(order[i], (unsigned)(j * W + i - row.off));
-            }
-        }
-    }
-    __syncthreads();
-    const int n = sh.count;
-    if (n <= CANDIDATES) {
-        // keys are unique: each one's place is the count of larger ones
-        for (int a = tid; a < n; a += blockDim.x) {
-            const uint64_t key = sh.list[a];
-            int place = 0;
-            for (int b = 0; b < n; ++b) place += sh.list[b] > key;
-            if (place < k) sh.best[place] = key;
-        }
-    } else {
-        uint64_t last = ~0ull;
-        for (int round = 0; round < k; ++round) {
-            uint64_t best = 0;
-            for (int q = tid >> 5; q < chosen; q += warps) {
-                const int64_t j0 = unit0 * 32 + ((int64_t)sh.chosen[q] << shift);
-                const int64_t j1 = min(j0 + ((int64_t)1 << shift), j_end);
-                for (int64_t j = j0 + lane; j < j1; j += 32) {
-                    float f[W];
-                    unpack(row.template load<Cache::KEEP>(j), f);
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        const unsigned order = order_of(f[i]);
-                        const uint64_t key = rank_key(order, (unsigned)(j * W + i - row.off));
-                        if (order > 0 && key < last && key > best) best = key;
+                for (int i = 0; i < W; ++i)
+                    if (order_of(f[i]) == tau) {
+                        if (at < k) sh.list[at] = rank_key(tau, (unsigned)(j * W + i - row.off));
+                        ++at;
                     }
-                }
+                have += all;
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(ALL, best, o));
-            __syncthreads();                    // the list is free: its entries are not used here
-            if (lane == 0) sh.list[tid >> 5] = best;
-            __syncthreads();
-            for (int w = 0; w < warps; ++w) best = max(best, sh.list[w]);
-            last = best;
-            if (tid == 0) sh.best[round] = best;
-            if (best == 0) break;
+            if (lane == 0) sh.count = max(above, min(have, k));
         }
+        __syncthreads();
+    }
+    // keys are unique: each one's place is the count of larger ones
+    const int n = sh.count;
+    for (int a = tid; a < n; a += blockDim.x) {
+        const uint64_t key = sh.list[a];
+        int place = 0;
+        for (int b = 0; b < n; ++b) place += sh.list[b] > key;
+        if (place < k) sh.best[place] = key;
     }
     __syncthreads();
 }
 
 // A block (SPLIT: one of a cluster's blocks, each with an equal share of the
-// units) per row.  Each warp takes UNITS accesses of 32 lanes at a time, its own
-// running maximum as the base; the groups' maxima for the alternatives come
-// from the same registers.  The bound is HBM (the row once).
+// units) per row.  Each lane takes UNITS accesses at a time and keeps its own
+// running maximum, base and sums, so the loop has no exchange between lanes; the
+// same maxima serve the choice of the alternatives.  The bound is HBM (the row
+// once) while an element costs under about 9 instructions: 16-bit maxima and the floor
+// are taken two at a time before unpacking, products and sums two at a time after.
 template <typename T, bool TOP, bool SPLIT>
-__global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p, int split,
-                                                                 int shift) {
+__global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p, int split) {
     constexpr int W = Row<T>::W;
     __shared__ RowShared sh;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, warps = blockDim.x >> 5;
     const int64_t r = SPLIT ? blockIdx.x / split : blockIdx.x;
-    const int part = SPLIT ? blockIdx.x % split : 0;
+    const int rank = SPLIT ? blockIdx.x % split : 0;
     const T* x = static_cast<const T*>(p.logits) + r * p.ld;
     const Row<T> row(x, p.vocab);
     const int64_t all_units = (row.end + 32 * W - 1) / (32 * W);
     const int64_t share = SPLIT ? (all_units + split - 1) / split : all_units;
-    const int64_t unit0 = part * share;
-    const int64_t units = max((int64_t)0, min(share, all_units - unit0));
+    Part part{rank * share, 0, warps};
+    part.units = max((int64_t)0, min(share, all_units - part.unit0));
     const float c = p.alpha * LOG2E;
-    const float lim = fminf(1e30f, 1e36f / c);      // |m| up to here: c m is far from overflow
+    // logits up to here: c x is rounded by less than 1/16, so that a difference of two
+    // equal ones, one of them rounded, stays small
+    const float lim = fminf(1e30f, 1e6f / c);
 
-    if (TOP) {
-        sh.group_max[tid] = 0;
-        __syncthreads();
-    }
+    // Masked logits, and all that are lower, count as `low`, far below the base: 2^t is
+    // 0 there and 0 * t is 0.  (Lanes that see nothing else count them in full, but
+    // lose them on the way to the row's base.)
+    const float low =
+        to_f32(from_f32<T>(std::is_same_v<T, __half> ? fmaxf(-lim, -65504.0f) : -lim));
+    Largest<T> top(low);
     Sums a{-INFINITY, 0.0f, 0.0f};
-    float base = base_of(a.m, c, lim);
-    for (int64_t t = (int64_t)w * UNITS; t < units; t += warps * UNITS) {
+    float base = base_of(a.m, c, low);
+    uint64_t s2 = pair(0.0f, 0.0f), u2 = s2;
+    const uint64_t c2 = pair(c, c);
+    for (int64_t t = (int64_t)w * UNITS; t < part.units; t += warps * UNITS) {
         Vec<T, W> v[UNITS];
-        const int64_t j0 = (unit0 + t) * 32 + lane;
-        if (t + UNITS <= units && row.whole(j0 - lane) && row.whole(j0 - lane + 32 * UNITS - 1)) {
+        const int64_t j0 = (part.unit0 + t) * 32 + lane;
+        if (t + UNITS <= part.units && row.whole(j0 - lane) &&
+            row.whole(j0 - lane + 32 * UNITS - 1)) {
 #pragma unroll
             for (int i = 0; i < UNITS; ++i)
                 v[i] = load_vec<TOP ? Cache::KEEP : Cache::STREAM, T, W>(row.from + (j0 + 32 * i) * W);
@@ -324,73 +382,71 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
 #pragma unroll
             for (int i = 0; i < UNITS; ++i)
                 v[i] = row.template load<Cache::KEEP>(
-                    t + i < units ? j0 + 32 * i : (all_units + i) * 32 + lane);
+                    t + i < part.units ? j0 + 32 * i : (all_units + i) * 32 + lane);
         }
-        float m = -INFINITY;
-        if (TOP && shift >= 5) {
 #pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                const float um = warp_max(vec_max(v[i]));
-                m = fmaxf(m, um);
-                if (lane == 0 && t + i < units) {
-                    unsigned* g = sh.group_max + ((t + i) >> (shift - 5));
-                    if (shift == 5) *g = order_of(um);
-                    else atomicMax(g, order_of(um));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                float gm = vec_max(v[i]);
-                if (TOP && t + i < units) {     // groups narrower than a unit
-                    for (int o = 1; o < 1 << shift; o <<= 1)
-                        gm = fmaxf(gm, __shfl_xor_sync(ALL, gm, o));
-                    if ((lane & ((1 << shift) - 1)) == 0)
-                        sh.group_max[((t + i) * 32 + lane) >> shift] = order_of(gm);
-                }
-                m = fmaxf(m, gm);
-            }
-            m = warp_max(m);
-        }
+        for (int i = 0; i < UNITS; ++i) top.see(v[i]);
+        const float m = top.value();
         if (m > a.m) {
-            const float next = base_of(m, c, lim), d = base - next, e = exp2_approx(d);
-            a.u = e * (a.u + (e > 0.0f ? d : 0.0f) * a.s);
-            a.s *= e;
+            const float next = base_of(m, c, low);
+            float s0, s1, u0, u1;
+            halves(s2, s0, s1);
+            halves(u2, u0, u1);
+            rebase(s0, u0, base - next);
+            rebase(s1, u1, base - next);
+            s2 = pair(s0, s1);
+            u2 = pair(u0, u1);
             a.m = m;
             base = next;
         }
+        const uint64_t b2 = pair(-base, -base);
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             float f[W];
-            unpack(v[i], f);
+            top.floor(v[i], f);
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                // far below the base 2^t is 0, and 0 * t must be 0 too; NaN stays NaN
-                const float d = max_nan(fmaf(f[e], c, -base), -200.0f);
-                const float q = exp2_approx(d);
-                a.s += q;
-                a.u = fmaf(q, d, a.u);
+            for (int e = 0; e < W; e += 2) {
+                const uint64_t d2 = fma2(pair(f[e], f[e + 1]), c2, b2);
+                float d0, d1;
+                halves(d2, d0, d1);
+                const uint64_t q2 = pair(exp2_approx(d0), exp2_approx(d1));
+                s2 = add2(s2, q2);
+                u2 = fma2(q2, d2, u2);
             }
         }
     }
-    a.s = warp_sum(a.s);
-    a.u = warp_sum(a.u);
+    {
+        float s0, s1, u0, u1;
+        halves(s2, s0, s1);
+        halves(u2, u0, u1);
+        a.s = s0 + s1;
+        a.u = u0 + u1;
+    }
+    const unsigned mine = order_of(top.value());
+    {
+        // the warp's lanes to one base
+        const float m = warp_max(a.m);
+        rebase(a.s, a.u, base - base_of(m, c, low));
+        a.m = m;
+        a.s = warp_sum(a.s);
+        a.u = warp_sum(a.u);
+    }
     if (lane == 0) sh.sums[w] = a;
     __syncthreads();
     if (tid == 0) {
         a = sh.sums[0];
-        for (int i = 1; i < warps; ++i) add(a, sh.sums[i], c, lim);
+        for (int i = 1; i < warps; ++i) add(a, sh.sums[i], c, low);
         sh.total = a;
     }
-    if (TOP) choose(sh, row, unit0, units, shift, p.top_k);
+    if (TOP) choose(sh, row, part, mine, p.top_k);
     __syncthreads();
     a = sh.total;
     if constexpr (SPLIT) {
         // the first block joins the parts in order
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
-        if (part == 0) {
-            for (int i = 1; i < split; ++i) add(a, cluster.map_shared_rank(&sh, i)->total, c, lim);
+        if (rank == 0) {
+            for (int i = 1; i < split; ++i) add(a, cluster.map_shared_rank(&sh, i)->total, c, low);
             if (TOP) {
                 const int n = split * p.top_k;      // at most one key per thread
                 uint64_t key = 0;
@@ -408,11 +464,13 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
             }
         }
         cluster.sync();
-        if (part != 0) return;
+        if (rank != 0) return;
     }
-    if (a.m > lim || (a.m < -lim && a.m > -INFINITY)) {
-        // a maximum that the base cannot follow (the type's lowest value throughout, +inf):
-        // the sums again, from the differences to it
+    const bool far = a.m > lim || ((a.m - low) * c < 200.0f && a.m > -INFINITY);
+    if (far) {
+        // a maximum that the base cannot follow (+inf, huge values) or that is not far above
+        // `low` (the type's lowest value throughout): the sums again, from the differences
+        // to it
         a.s = a.u = 0.0f;
         for (int64_t i = tid; i < p.vocab; i += blockDim.x) {
             const float v = to_f32(x[i]);
@@ -431,14 +489,11 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
             a.s += sh.sums[i].s;
             a.u += sh.sums[i].u;
         }
-        base = a.m * c;
-    } else {
-        base = base_of(a.m, c, lim);
     }
     // alpha m carries the bulk; the rest is what the base's rounding left of c m, and log2 S
-    const bool none = a.s == 0.0f;                  // nothing unmasked (NaN is not 0)
+    const bool none = a.m == -INFINITY && a.s == a.s;   // nothing unmasked, and no NaN
     const float log_s = log2f(a.s);
-    const float left = a.m > lim || a.m < -lim ? 0.0f : fmaf(-a.m, c, base);
+    const float left = far ? 0.0f : fmaf(-a.m, c, base_of(a.m, c, low));
     const float lse = none ? -INFINITY
                       : a.m == -INFINITY ? NAN      // NaNs alone
                                          : fmaf(p.alpha, a.m, LN2 * (log_s + left));
@@ -473,8 +528,6 @@ cudaError_t launch_forward(const LogprobParams& p, int num_sms, cudaStream_t st)
     // A warp per 8 units, so that narrow rows leave room for other rows' blocks.
     int warps = LP_WARPS;
     while (warps > 1 && share < 8 * warps / 2 && split == 1) warps /= 2;
-    int shift = 0;
-    while ((share * 32 + (1LL << shift) - 1) >> shift > 32 * warps) ++shift;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.rows * split));
     cfg.blockDim = dim3(32 * warps);
@@ -488,7 +541,7 @@ cudaError_t launch_forward(const LogprobParams& p, int num_sms, cudaStream_t st)
     auto kernel = p.top_k > 0
                       ? (split > 1 ? logprob_rows<T, true, true> : logprob_rows<T, true, false>)
                       : (split > 1 ? logprob_rows<T, false, true> : logprob_rows<T, false, false>);
-    return cudaLaunchKernelEx(&cfg, kernel, p, split, shift);
+    return cudaLaunchKernelEx(&cfg, kernel, p, split);
 }
 
 // ---- gradient ---------------------------------------------------------------------------
@@ -497,12 +550,14 @@ constexpr int LG_THREADS = 256;
 constexpr int LG_BATCH = 4;          // accesses in flight per thread
 
 // dx = p * (-(up + de * entropy) - de * q) (+ up at the target), with alpha in up
-// and de, q = alpha x - lse and p = exp(q).  Blocks (row, columns); W == 1 where
-// logits and dlogits lie differently against 16-byte boundaries.  The bound is HBM
-// (read x, write dx).
+// and de, q = alpha x - lse and p = exp(q).  A row takes `pieces` consecutive
+// blocks, so that blocks in flight together work on neighbouring memory; W == 1
+// where logits and dlogits lie differently against 16-byte boundaries.  The
+// bound is HBM (read x, write dx).
 template <typename T, int W>
-__global__ __launch_bounds__(LG_THREADS) void logprob_grad_rows(LogprobGradParams p) {
-    const int64_t r = blockIdx.x;
+__global__ __launch_bounds__(LG_THREADS) void logprob_grad_rows(LogprobGradParams p, int pieces) {
+    const int64_t r = blockIdx.x / pieces;
+    const int piece = blockIdx.x % pieces;
     const T* x = static_cast<const T*>(p.logits) + r * p.ld;
     T* dx = static_cast<T*>(p.dlogits) + r * p.ld_out;
     const Row<T> row(x, p.vocab);
@@ -518,38 +573,44 @@ __global__ __launch_bounds__(LG_THREADS) void logprob_grad_rows(LogprobGradParam
     const float de = p.dentropy ? p.alpha * p.dentropy[r] : 0.0f;
     const float k = p.dentropy ? -fmaf(de, p.entropy[r], up) : -up;
     const int64_t at_target = has ? (int64_t)target + off : -1;
-    for (int64_t j0 = (int64_t)blockIdx.y * step * LG_BATCH + threadIdx.x; j0 < nvec;
-         j0 += (int64_t)gridDim.y * step * LG_BATCH) {
-        float f[LG_BATCH][W];
+    const bool empty = lse == -INFINITY;
+    for (int64_t j0 = (int64_t)piece * step * LG_BATCH + threadIdx.x; j0 < nvec;
+         j0 += (int64_t)pieces * step * LG_BATCH) {
+        Vec<T, W> v[LG_BATCH];       // packed until all are on their way
 #pragma unroll
         for (int b = 0; b < LG_BATCH; ++b) {
             const int64_t j = j0 + (int64_t)b * step;
             if (j >= nvec) continue;
-            if constexpr (W > 1) unpack(row.template load<Cache::STREAM>(j), f[b]);
-            else f[b][0] = to_f32(x[j]);
+            if constexpr (W > 1) v[b] = row.template load<Cache::STREAM>(j);
+            else v[b].w = x[j];
         }
 #pragma unroll
         for (int b = 0; b < LG_BATCH; ++b) {
             const int64_t j = j0 + (int64_t)b * step;
             if (j >= nvec) continue;
+            float f[W];
+            unpack(v[b], f);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
                 // masked: p is 0, and 0 times the rest must be 0 too; NaN stays NaN
-                const float q = max_nan(fmaf(p.alpha, f[b][i], -lse), -200.0f);
-                const float e = exp2_approx(q * LOG2E);
-                f[b][i] = lse == -INFINITY ? 0.0f : e * fmaf(-de, q, k);
+                const float q = max_nan(fmaf(p.alpha, f[i], -lse), -200.0f);
+                f[i] = exp2_approx(q * LOG2E) * fmaf(-de, q, k);
             }
-            if (at_target >= j * W && at_target < (j + 1) * W && lse != -INFINITY)
+            const int64_t hit = at_target - j * W;
+            if (hit >= 0 && hit < W)
 #pragma unroll
                 for (int i = 0; i < W; ++i)
-                    if (j * W + i == at_target) f[b][i] += up;
+                    if (i == hit) f[i] += up;
+            if (empty)
+#pragma unroll
+                for (int i = 0; i < W; ++i) f[i] = 0.0f;
             if (W == 1 || row.whole(j)) {
-                store_vec<Cache::STREAM, T, W>(dx + j * W, f[b]);
+                store_vec<Cache::STREAM, T, W>(dx + j * W, f);
             } else {
 #pragma unroll
                 for (int i = 0; i < W; ++i)
                     if (j * W + i >= off && j * W + i < end)
-                        dx[j * W + i] = from_f32<T>(f[b][i]);
+                        dx[j * W + i] = from_f32<T>(f[i]);
             }
         }
     }
@@ -560,9 +621,9 @@ cudaError_t launch_grad(const LogprobGradParams& p, cudaStream_t st) {
     const int64_t nvec = (p.vocab + 2 * (W - 1)) / W;                  // at most, by alignment
     int threads = LG_THREADS;
     while (threads > 64 && nvec <= threads / 2 * LG_BATCH) threads /= 2;
-    const int64_t pieces = (nvec + threads * LG_BATCH - 1) / (threads * LG_BATCH);
-    const dim3 grid((unsigned)p.rows, (unsigned)std::min<int64_t>(pieces, 65535));
-    logprob_grad_rows<T, W><<<grid, threads, 0, st>>>(p);
+    const int64_t whole = (nvec + threads * LG_BATCH - 1) / (threads * LG_BATCH);
+    const int pieces = (int)std::max<int64_t>(1, std::min<int64_t>(whole, 0x7fffffff / p.rows));
+    logprob_grad_rows<T, W><<<(unsigned)(p.rows * pieces), threads, 0, st>>>(p, pieces);
     return cudaGetLastError();
 }
 

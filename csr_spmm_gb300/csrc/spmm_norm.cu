@@ -63,70 +63,98 @@ __device__ __forceinline__ float row_sum(float x, float* s, int row, int warps) 
 
 // The row in registers: `warps` warps hold it in K accesses of W elements per
 // lane, so x is read once and the second pass over it costs no memory.  Several
-// narrow rows share a block.  The bound is HBM (read x, write y).
-template <typename T, typename P, int W, int K>
-__global__ __launch_bounds__(1024) void norm_rows(NormParams p, int warps, int nvec) {
+// narrow rows share a block.  With STAGES > 0 the row's warps walk the rows with
+// a fixed stride and keep STAGES - 1 rows ahead on their way to shared memory,
+// each lane's accesses in slots of its own.  The bound is HBM (read x, write y).
+template <typename T, typename P, int W, int K, int STAGES>
+__global__ __launch_bounds__(1024) void norm_rows(NormParams p, int warps, int nvec,
+                                                  int64_t stride) {
     __shared__ float s[2][32];
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
     const int threads = warps * 32;
     const int in_block = threadIdx.x / threads, tid = threadIdx.x % threads;
-    const int64_t r = (int64_t)blockIdx.x * (blockDim.x / threads) + in_block;
-    if (r >= p.rows) return;
-    const T* x = static_cast<const T*>(p.x) + r * p.ldx;
-    Vec<T, W> held[K];
-    float sum = 0.0f;
+    const T* xs = static_cast<const T*>(p.x);
+    int64_t r = (int64_t)blockIdx.x * (blockDim.x / threads) + in_block;
+    Vec<T, W>* ring = reinterpret_cast<Vec<T, W>*>(ring_bytes) + threadIdx.x;
+    auto copy = [&](int64_t row, int stage) {
+        if constexpr (STAGES > 0) {
+            if (row < p.rows)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (k * threads + tid < nvec)
-            held[k] = load_vec<Cache::STREAM, T, W>(x + (int64_t)(k * threads + tid) * W);
-    // one access per lane is the case of few rows, where latency counts: the
-    // parameters are on their way during the sums
-    float w0[W], b0[W];
-    if constexpr (K == 1)
-        if (tid < nvec) {
-            params<P, W>(p.weight, tid * W, 1.0f, w0);
-            params<P, W>(p.bias, tid * W, 0.0f, b0);
+                for (int k = 0; k < K; ++k)
+                    if (k * threads + tid < nvec)
+                        copy_async<T, W>(ring + (stage * K + k) * blockDim.x,
+                                         xs + row * p.ldx + (int64_t)(k * threads + tid) * W);
+            copies_issued();
         }
+    };
+    for (int i = 0; i < STAGES - 1; ++i) copy(r + i * stride, i);
+    int stage = 0;
+    for (; r < p.rows; r += stride) {
+        Vec<T, W> held[K];
+        if constexpr (STAGES > 0) {
+            copies_wait<(STAGES > 1 ? STAGES - 2 : 0)>();
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (k * threads + tid < nvec) {
-            float f[W];
+            for (int k = 0; k < K; ++k) held[k] = ring[(stage * K + k) * blockDim.x];
+            copy(r + (STAGES - 1) * stride, stage == 0 ? STAGES - 1 : stage - 1);
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k * threads + tid < nvec)
+                    held[k] = load_vec<Cache::STREAM, T, W>(xs + r * p.ldx +
+                                                            (int64_t)(k * threads + tid) * W);
+        }
+        // one access per lane is the case of few rows, where latency counts: the
+        // parameters are on their way during the sums
+        float w0[W], b0[W];
+        if constexpr (K == 1)
+            if (tid < nvec) {
+                params<P, W>(p.weight, tid * W, 1.0f, w0);
+                params<P, W>(p.bias, tid * W, 0.0f, b0);
+            }
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (k * threads + tid < nvec) {
+                float f[W];
+                unpack(held[k], f);
+#pragma unroll
+                for (int i = 0; i < W; ++i) sum += f[i];
+            }
+        float* slot = s[0] + in_block * warps;
+        const float mean = row_sum(sum, slot, in_block, warps) / (float)p.dim;
+        sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (k * threads + tid < nvec) {
+                float f[W];
+                unpack(held[k], f);
+#pragma unroll
+                for (int i = 0; i < W; ++i) sum += (f[i] - mean) * (f[i] - mean);
+            }
+        slot = s[1] + in_block * warps;
+        const float var = row_sum(sum, slot, in_block, warps) / (float)p.dim;
+        const float rstd = 1.0f / sqrtf(var + p.eps);
+        T* y = static_cast<T*>(p.y) + r * p.ldy;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int at = k * threads + tid;
+            if (at >= nvec) continue;
+            float f[W], w[W], b[W];
             unpack(held[k], f);
+            if constexpr (K > 1) {
+                params<P, W>(p.weight, at * W, 1.0f, w);
+                params<P, W>(p.bias, at * W, 0.0f, b);
+            }
 #pragma unroll
-            for (int i = 0; i < W; ++i) sum += f[i];
+            for (int i = 0; i < W; ++i)
+                f[i] = (f[i] - mean) * rstd * (K == 1 ? w0[i] : w[i]) + (K == 1 ? b0[i] : b[i]);
+            store_vec<Cache::STREAM, T, W>(y + (int64_t)at * W, f);
         }
-    float* slot = s[0] + in_block * warps;
-    const float mean = row_sum(sum, slot, in_block, warps) / (float)p.dim;
-    sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (k * threads + tid < nvec) {
-            float f[W];
-            unpack(held[k], f);
-#pragma unroll
-            for (int i = 0; i < W; ++i) sum += (f[i] - mean) * (f[i] - mean);
+        if (tid == 0) {
+            if (p.mean) p.mean[r] = mean;
+            if (p.rstd) p.rstd[r] = rstd;
         }
-    slot = s[1] + in_block * warps;
-    const float var = row_sum(sum, slot, in_block, warps) / (float)p.dim;
-    const float rstd = 1.0f / sqrtf(var + p.eps);
-    T* y = static_cast<T*>(p.y) + r * p.ldy;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int at = k * threads + tid;
-        if (at >= nvec) continue;
-        float f[W], w[W], b[W];
-        unpack(held[k], f);
-        if constexpr (K > 1) {
-            params<P, W>(p.weight, at * W, 1.0f, w);
-            params<P, W>(p.bias, at * W, 0.0f, b);
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            f[i] = (f[i] - mean) * rstd * (K == 1 ? w0[i] : w[i]) + (K == 1 ? b0[i] : b[i]);
-        store_vec<Cache::STREAM, T, W>(y + (int64_t)at * W, f);
-    }
-    if (tid == 0) {
-        if (p.mean) p.mean[r] = mean;
-        if (p.rstd) p.rstd[r] = rstd;
     }
 }
 
@@ -158,10 +186,14 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_any(NormParams p) {
 }
 
 // dx, and this block's share of dweight and dbias, in one pass over dy and x: a
-// row's `warps` warps hold it in registers, walk the rows with a fixed stride
-// (the next row's accesses are issued before this row's sums), and keep their
-// columns' sums of dy * xhat and dy in registers to the end.  The bound is HBM
-// (read dy and x, write dx).  part: [slices][2][dim].
+// row's `warps` warps hold it in registers, walk the rows with a fixed stride, and keep their
+// columns' sums of dy * xhat and dy in registers to the end.  The rows ahead are
+// on their way to shared memory, each lane's accesses in slots of its own
+// (single 16-bit elements cannot be copied so: the next row waits in registers).
+// The bound is HBM (read dy and x, write dx).  part: [slices][2][dim].
+// Stages of the ring: what 512 threads can have of the 227 KB, four at most.
+template <typename T, int W, int K>
+constexpr int GRAD_STAGES = sizeof(T) * W * K > 32 ? 3 : 4;
 template <typename T, typename P, int W, int K>
 __global__ __launch_bounds__(NORM_GRAD_THREADS) void norm_grad_rows(NormGradParams p, int warps,
                                                                     int nvec, int slices) {
@@ -176,19 +208,35 @@ __global__ __launch_bounds__(NORM_GRAD_THREADS) void norm_grad_rows(NormGradPara
     // 16 elements a lane leave no registers for the weights in binary32 (W = 4) and
     // for single accesses (W = 1): those read them again for each row, from L1
     constexpr bool HOLD = W * K < 16 || W == 8;
+    constexpr bool RING = can_copy_async<T, W>;
+    constexpr int STAGES = GRAD_STAGES<T, W, K>;
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    Vec<T, W>* ring = reinterpret_cast<Vec<T, W>*>(ring_bytes) + threadIdx.x;
     Vec<T, W> x[K], dy[K];
     float weight[HOLD ? K : 1][W], dw[K][W], db[K][W];
-    auto fetch = [&](int64_t r) {
+    // sends for row r: to a stage of the ring, or to the registers
+    auto fetch = [&](int64_t r, int stage) {
+        if (r < p.rows)
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int at = k * threads + tid;
-            if (at < nvec) {
-                x[k] = load_vec<Cache::STREAM, T, W>(xs + r * p.ldx + (int64_t)at * W);
-                dy[k] = load_vec<Cache::STREAM, T, W>(dys + r * p.ld_dy + (int64_t)at * W);
+            for (int k = 0; k < K; ++k) {
+                const int at = k * threads + tid;
+                if (at >= nvec) continue;
+                const T* xr = xs + r * p.ldx + (int64_t)at * W;
+                const T* dyr = dys + r * p.ld_dy + (int64_t)at * W;
+                if constexpr (RING) {
+                    copy_async<T, W>(ring + (stage * 2 * K + k) * blockDim.x, xr);
+                    copy_async<T, W>(ring + (stage * 2 * K + K + k) * blockDim.x, dyr);
+                } else {
+                    x[k] = load_vec<Cache::STREAM, T, W>(xr);
+                    dy[k] = load_vec<Cache::STREAM, T, W>(dyr);
+                }
             }
-        }
+        if constexpr (RING) copies_issued();
     };
-    fetch(slice);
+    if constexpr (RING)
+        for (int i = 0; i < STAGES - 1; ++i) fetch(slice + (int64_t)i * slices, i);
+    else
+        fetch(slice, 0);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -196,8 +244,18 @@ __global__ __launch_bounds__(NORM_GRAD_THREADS) void norm_grad_rows(NormGradPara
         if (HOLD && k * threads + tid < nvec)
             params<P, W>(p.weight, (int64_t)(k * threads + tid) * W, 1.0f, weight[HOLD ? k : 0]);
     }
-    int turn = 0;
+    int turn = 0, stage = 0;
     for (int64_t r = slice; r < p.rows; r += slices) {
+        if constexpr (RING) {
+            copies_wait<STAGES - 2>();
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                x[k] = ring[(stage * 2 * K + k) * blockDim.x];
+                dy[k] = ring[(stage * 2 * K + K + k) * blockDim.x];
+            }
+            fetch(r + (int64_t)(STAGES - 1) * slices, stage == 0 ? STAGES - 1 : stage - 1);
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
+        }
         const float mean = p.mean[r], rstd = p.rstd[r];
         float xh[K][W], g[K][W];
         float a = 0.0f, b = 0.0f;
@@ -218,7 +276,7 @@ __global__ __launch_bounds__(NORM_GRAD_THREADS) void norm_grad_rows(NormGradPara
                     b += g[k][i] * xh[k][i];
                 }
             }
-        if (r + slices < p.rows) fetch(r + slices);
+        if constexpr (!RING) fetch(r + slices, 0);
         a = warp_sum(a);
         b = warp_sum(b);
         if (warps > 1) {
@@ -362,13 +420,26 @@ int64_t slices_rows(int64_t rows, int warps, int num_sms, int sm_warps) {
 }
 constexpr int SM_WARPS_MOST = 32;    // 64 registers a thread: up to 4 elements per lane
 
-template <typename T, typename P, int W, int K>
-cudaError_t norm_launch(const NormParams& p, cudaStream_t st) {
+template <typename... KArgs>
+cudaError_t allow_shared(void (*kernel)(KArgs...), size_t bytes) {
+    return bytes <= 32768 ? cudaSuccess
+                          : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)bytes);
+}
+
+template <typename T, typename P, int W, int K, int STAGES>
+cudaError_t norm_launch(const NormParams& p, int num_sms, cudaStream_t st) {
     const int nvec = (int)(p.dim / W);
     const int warps = warps_for(nvec, K);
     const int rows = std::max(1, 8 / warps);          // at least 256 threads
-    norm_rows<T, P, W, K><<<(unsigned)((p.rows + rows - 1) / rows), rows * warps * 32, 0, st>>>(
-        p, warps, nvec);
+    int64_t blocks = (p.rows + rows - 1) / rows;
+    // with a ring: as many blocks as the SMs hold at 64 registers a thread
+    if (STAGES > 0) blocks = std::min<int64_t>(blocks, (int64_t)num_sms * (32 / (rows * warps)));
+    const size_t shared = (size_t)STAGES * K * rows * warps * 32 * sizeof(Vec<T, W>);
+    auto kernel = norm_rows<T, P, W, K, STAGES>;
+    cudaError_t e = allow_shared(kernel, shared);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)blocks, rows * warps * 32, shared, st>>>(p, warps, nvec, blocks * rows);
     return cudaGetLastError();
 }
 
@@ -379,8 +450,14 @@ cudaError_t norm_grad_launch(const NormGradParams& p, int num_sms, cudaStream_t 
     const int rows = std::max(1, 4 / warps);          // at least 128 threads
     constexpr int SM_WARPS = W * K <= 4 ? SM_WARPS_MOST : SM_WARPS_MOST / 2;
     *slices = (int)slices_rows(p.rows, warps, num_sms, SM_WARPS);
-    norm_grad_rows<T, P, W, K><<<(*slices + rows - 1) / rows, rows * warps * 32, 0, st>>>(
-        p, warps, nvec, *slices);
+    const size_t shared = can_copy_async<T, W>
+                              ? (size_t)GRAD_STAGES<T, W, K> * 2 * K * rows * warps * 32 * sizeof(Vec<T, W>)
+                              : 0;
+    auto kernel = norm_grad_rows<T, P, W, K>;
+    cudaError_t e = allow_shared(kernel, shared);
+    if (e != cudaSuccess) return e;
+    kernel<<<(*slices + rows - 1) / rows, rows * warps * 32, shared, st>>>(p, warps, nvec,
+                                                                          *slices);
     return cudaGetLastError();
 }
 
@@ -402,11 +479,11 @@ cudaError_t launch_layer_norm(spmm_type_t type, spmm_type_t param_type, const No
         if (wide) {
             const int64_t nvec = p.dim / W;
             if (nvec <= 1024 && (p.rows <= 2 * num_sms || nvec <= 32))
-                return norm_launch<T, P, W, 1>(p, st);
-            if (nvec <= 4096) return norm_launch<T, P, W, 4>(p, st);
+                return norm_launch<T, P, W, 1, 0>(p, num_sms, st);
+            if (nvec <= 4096) return norm_launch<T, P, W, 4, 3>(p, num_sms, st);
         } else {
-            if (p.dim <= 4096) return norm_launch<T, P, 1, 4>(p, st);
-            if (p.dim <= 16384) return norm_launch<T, P, 1, 16>(p, st);
+            if (p.dim <= 4096) return norm_launch<T, P, 1, 4, 0>(p, num_sms, st);
+            if (p.dim <= 16384) return norm_launch<T, P, 1, 16, 0>(p, num_sms, st);
         }
         const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
         norm_any<T, P><<<blocks, NORM_THREADS, 0, st>>>(p);
