@@ -84,7 +84,8 @@ struct NormGradParams {
     int64_t ld_dx;
     void* dweight;           // or NULL
     void* dbias;             // or NULL
-    float* part;             // scratch: partial sums
+    float* part;             // scratch: partial sums of dweight and dbias
+    float* means;            // scratch: two means per row (set by the launch)
 };
 size_t norm_grad_scratch(int64_t rows, int64_t dim, int num_sms);
 cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,

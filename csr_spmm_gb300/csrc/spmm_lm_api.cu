@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t MAX_COUNT = INT_MAX - 1;      // rows, tokens and columns: 32-bit indices
 constexpr int64_t MAX_TOKENS = 1LL << 30;       // sorted tokens: room for padding in 32 bits
+constexpr int64_t MAX_WIDTH = 1LL << 30;        // columns of a layer norm, likewise
 
 inline bool bad_type(spmm_type_t t) { return t != SPMM_F32 && t != SPMM_F16 && t != SPMM_BF16; }
 // Parameters and gradients have the operands' type or binary32.
@@ -90,7 +91,7 @@ spmm_status_t spmm_layer_norm(spmm_handle_t h, spmm_type_t type, spmm_type_t par
                               const void* weight, const void* bias, float eps, void* y,
                               int64_t ldy, float* mean, float* rstd, void* stream) {
     if (!h || bad_pair(type, param_type) || bad_count(rows, MAX_COUNT) ||
-        bad_count(dim, MAX_COUNT) || !(eps >= 0.0f))
+        bad_count(dim, MAX_WIDTH) || !(eps >= 0.0f))
         return SPMM_ERR_INVALID_ARGUMENT;
     if (short_ld(ldx, dim) || short_ld(ldy, dim)) return SPMM_ERR_DIMENSION_MISMATCH;
     if (rows == 0 || dim == 0) return SPMM_OK;
@@ -109,7 +110,7 @@ spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_
                                    int64_t rows, int64_t dim, void* dx, int64_t ld_dx,
                                    void* dweight, void* dbias, void* stream) {
     if (!h || bad_pair(type, param_type) || bad_count(rows, MAX_COUNT) ||
-        bad_count(dim, MAX_COUNT))
+        bad_count(dim, MAX_WIDTH))
         return SPMM_ERR_INVALID_ARGUMENT;
     if (short_ld(ld_dy, dim) || short_ld(ldx, dim) || short_ld(ld_dx, dim))
         return SPMM_ERR_DIMENSION_MISMATCH;
@@ -119,12 +120,11 @@ spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_
     spmm_status_t s = lm_device(h, &sms);
     if (s != SPMM_OK) return s;
     char* scratch = nullptr;
-    if (dweight || dbias) {
-        s = lm_scratch(h, norm_grad_scratch(rows, dim, sms), &scratch);
-        if (s != SPMM_OK) return s;
-    }
-    const NormGradParams p{dy, ld_dy, x,  ldx,   mean,    rstd,  weight,
-                           rows, dim, dx, ld_dx, dweight, dbias, reinterpret_cast<float*>(scratch)};
+    s = lm_scratch(h, norm_grad_scratch(rows, dim, sms), &scratch);
+    if (s != SPMM_OK) return s;
+    const NormGradParams p{dy, ld_dy, x,     ldx,     mean,  rstd, weight, rows,
+                           dim, dx,   ld_dx, dweight, dbias, reinterpret_cast<float*>(scratch),
+                           nullptr};
     return launched(launch_layer_norm_grad(type, param_type, p, sms,
                                            reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -27,7 +27,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 // W consecutive elements as they lie in memory: W > 1 in 32-bit words, so that
 // 16-bit elements stay packed in registers until they are used.
 template <typename T, int W>
-struct alignas(sizeof(T) * W % 16 == 0 ? 16 : 4) Vec {
+struct alignas(sizeof(T) * W % 16 == 0 ? 16 : sizeof(T) * W) Vec {
     static constexpr int WORDS = (int)sizeof(T) * W / 4;
     uint32_t w[WORDS];
 };
@@ -72,11 +72,17 @@ __device__ __forceinline__ void unpack(const Vec<T, W>& r, float (&f)[W]) {
 // is read once.
 enum class Cache { KEEP, STREAM };
 
-// W consecutive elements: 16-byte accesses when W > 1, one element otherwise.
+// W consecutive elements: 16-byte accesses (one of 8 bytes for four 16-bit elements)
+// when W > 1, one element otherwise.
 template <Cache C, typename T, int W>
 __device__ __forceinline__ Vec<T, W> load_vec(const T* p) {
     Vec<T, W> r;
-    if constexpr (W > 1) {
+    if constexpr (sizeof(T) * W == 8) {
+        const uint2* from = reinterpret_cast<const uint2*>(p);
+        const uint2 u = C == Cache::STREAM ? __ldcs(from) : *from;
+        r.w[0] = u.x;
+        r.w[1] = u.y;
+    } else if constexpr (W > 1) {
         static_assert(sizeof(T) * W % 16 == 0);
         const uint4* from = reinterpret_cast<const uint4*>(p);
 #pragma unroll
@@ -97,12 +103,17 @@ __device__ __forceinline__ Vec<T, W> load_vec(const T* p) {
 template <Cache C, typename T, int W>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[W]) {
     if constexpr (W > 1) {
-        static_assert(sizeof(T) * W % 16 == 0);
+        static_assert(sizeof(T) * W % 16 == 0 || sizeof(T) * W == 8);
         uint32_t w[Vec<T, W>::WORDS];
 #pragma unroll
         for (int i = 0; i < Vec<T, W>::WORDS; ++i) {
             if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
             else w[i] = pack_word(f + 2 * i, T{});
+        }
+        if constexpr (sizeof(T) * W == 8) {
+            const uint2 u = make_uint2(w[0], w[1]);
+            if (C == Cache::STREAM) __stcs(reinterpret_cast<uint2*>(p), u);
+            else *reinterpret_cast<uint2*>(p) = u;
         }
         uint4* to = reinterpret_cast<uint4*>(p);
 #pragma unroll

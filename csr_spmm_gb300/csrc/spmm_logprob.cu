@@ -165,111 +165,146 @@ __device__ __forceinline__ void rebase(float& s, float& u, float d) {
     u = e * fmaf(fmaxf(d, -200.0f), s, u);      // no weight is left long before -200
     s *= e;
 }
-__device__ __forceinline__ void add(Sums& a, Sums b, float c, float low) {
-    const float m = fmaxf(a.m, b.m);
-    const float base = base_of(m, c, low);
-    rebase(a.s, a.u, base_of(a.m, c, low) - base);
-    rebase(b.s, b.u, base_of(b.m, c, low) - base);
-    a.m = m;
-    a.s += b.s;
-    a.u += b.u;
+// The warp's lanes' sums, each from its own base, to the base of their maximum.
+__device__ __forceinline__ Sums join(Sums a, float c, float low) {
+    const float m = warp_max(a.m);
+    rebase(a.s, a.u, base_of(a.m, c, low) - base_of(m, c, low));
+    return {m, warp_sum(a.s), warp_sum(a.u)};
 }
 
 struct RowShared {
     Sums sums[LP_WARPS];
     Sums total;                                 // this block's part of the row
     uint64_t best[SPMM_TOP_MAX];                // its alternatives, largest first (0: none)
-    unsigned chosen[32 * LP_WARPS];             // lanes whose logits hold the alternatives
+    unsigned short chosen[32 * LP_WARPS * UNITS];   // groups that hold the alternatives
     int chosen_count;
     int count;
     uint64_t list[CANDIDATES];
 };
 
 // How a block's threads share its part of a row: units of 32 accesses, each warp
-// UNITS at a time.  Thread t takes the accesses j0 + i * 32 + lane of its turns.
+// UNITS at a time.  The i-th accesses of thread t's turns are group t * UNITS + i.
 struct Part {
     int64_t unit0, units;
     int warps;
     __device__ int64_t turns() const { return (units + (int64_t)warps * UNITS - 1) / (warps * UNITS); }
-    // the q-th access of thread t (one past the end of its part: -1)
-    __device__ int64_t access(int t, int64_t q) const {
-        const int64_t unit = (q / UNITS * warps + t / 32) * UNITS + q % UNITS;
-        return unit < units ? (unit0 + unit) * 32 + t % 32 : -1;
+    // the q-th access of group g (past the end of the part: -1)
+    __device__ int64_t access(int g, int64_t q) const {
+        const int64_t unit = (q * warps + g / (32 * UNITS)) * UNITS + g % UNITS;
+        return unit < units ? (unit0 + unit) * 32 + g / UNITS % 32 : -1;
     }
 };
 
-// Adds an access's elements of order >= least to the list of candidates.
+// Adds the elements of order >= least among the accesses of the chosen groups to
+// the list of candidates.  The block's threads share those accesses, four at a time.
 template <typename T>
-__device__ __forceinline__ void collect(RowShared& sh, const Row<T>& row, int64_t j, unsigned least) {
+__device__ void collect(RowShared& sh, const Row<T>& row, const Part& part, int chosen,
+                        unsigned least) {
     constexpr int W = Row<T>::W;
-    float f[W];
-    unpack(row.template load<Cache::KEEP>(j), f);
+    // in values: NaN and -inf compare false, and what is no number's order means all
+    const float from = least > 0x00800000u ? value_of(least) : -3.402823466e38f;
+    const int own = (int)part.turns();              // accesses of a group, at most
+    const int all = chosen * own;
+    for (int i0 = threadIdx.x; i0 < all; i0 += 4 * blockDim.x) {
+        Vec<T, W> v[4];
+        int64_t j[4];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const unsigned order = order_of(f[i]);
-        if (order < least) continue;
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < CANDIDATES) sh.list[at] = rank_key(order, (unsigned)(j * W + i - row.off));
+        for (int b = 0; b < 4; ++b) {
+            const int i = i0 + b * blockDim.x;
+            j[b] = i < all ? part.access(sh.chosen[i / own], i % own) : -1;
+            if (j[b] >= 0) v[b] = row.template load<Cache::KEEP>(j[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (j[b] < 0) continue;
+            Largest<T> top(0.0f);
+            top.see(v[b]);
+            if (!(top.value() >= from)) continue;
+            float f[W];
+            unpack(v[b], f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                if (!(f[i] >= from)) continue;
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < CANDIDATES)
+                    sh.list[at] = rank_key(order_of(f[i]), (unsigned)(j[b] * W + i - row.off));
+            }
+        }
     }
 }
 
 // The alternatives of this block's part of the row, into sh.best.
 //
-// `mine` is the order of the largest of this thread's logits.  tau, the k-th largest
-// of the threads' values, is a lower bound of the k-th largest logit, and every
-// logit that reaches it belongs to a thread whose own largest does.  So a second look
-// (in L2) at the logits of those threads, k of them unless some are equal, gives a
-// short list that holds the alternatives; its entries are ranked by counting.
-// When more than CANDIDATES logits reach tau, nearly all must equal it: the list is
-// then made of those above tau, and the first equal ones in index order.
+// group[i] is the order of the largest logit of this thread's i-th group.  A number tau
+// that the largest logits of k threads reach is a lower bound of the k-th largest
+// logit, and every logit that reaches it belongs to a group whose largest does.  So a
+// second look (in L2) at those groups, little more than k of the block's 1024, gives
+// a short list that holds the alternatives; its entries are ranked by counting.
+// When more than CANDIDATES logits reach tau, it is raised to the k-th largest of the
+// threads' largest, which nearly all of them must equal then: the list is made of those
+// above tau, and the first equal ones in index order.
 template <typename T>
-__device__ void choose(RowShared& sh, const Row<T>& row, const Part& part, unsigned mine, int k) {
+__device__ void choose(RowShared& sh, const Row<T>& row, const Part& part,
+                       const unsigned (&group)[UNITS], int k) {
     constexpr int W = Row<T>::W;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    // the largest number that the values of at least k threads reach, bit by bit (a
-    // 16-bit logit has only the upper bits; 0: fewer than k have any)
-    unsigned tau = 0;
-    constexpr int LOW = sizeof(T) == 4 ? 0 : std::is_same_v<T, __half> ? 13 : 16;
-    for (int bit = 31; bit >= LOW; --bit) {
-        const unsigned next = tau | 1u << bit;
-        if (__syncthreads_count(mine >= next) >= k) tau = next;
+    unsigned mine = 0;
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) mine = max(mine, group[i]);
+    // tau: bit by bit below what all threads' values have in common, until exactly k
+    // reach it (0: fewer than k have any)
+    const unsigned wmax = __reduce_max_sync(ALL, mine), wmin = __reduce_min_sync(ALL, mine);
+    if (lane == 0) sh.list[w] = (uint64_t)wmax << 32 | wmin;
+    __syncthreads();
+    unsigned most = wmax, fewest = wmin;
+    for (int i = 0; i < part.warps; ++i) {
+        most = max(most, (unsigned)(sh.list[i] >> 32));
+        fewest = min(fewest, (unsigned)sh.list[i]);
     }
-    // of negative logits the lower bits are all set
-    if (LOW > 0 && tau > 0 && tau < 0x80000000u) tau |= (1u << LOW) - 1;
+    int bit = most == fewest ? -1 : 31 - __clz(most ^ fewest);
+    unsigned tau = bit < 0 ? most : bit == 31 ? 0 : most >> (bit + 1) << (bit + 1);
+    int reach = 0;
+    for (; bit >= 0 && reach != k; --bit) {
+        const unsigned next = tau | 1u << bit;
+        const int n = __syncthreads_count(mine >= next);
+        if (n < k) continue;
+        tau = next;
+        reach = n;
+    }
     if (tid < k) sh.best[tid] = 0;
     if (tid == 0) sh.chosen_count = sh.count = 0;
     __syncthreads();
     const unsigned least = max(tau, 1u);
-    if (mine >= least) sh.chosen[atomicAdd(&sh.chosen_count, 1)] = tid;
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i)
+        if (group[i] >= least)
+            sh.chosen[atomicAdd(&sh.chosen_count, 1)] = (unsigned short)(tid * UNITS + i);
     __syncthreads();
     const int chosen = sh.chosen_count;
-    const int64_t own = part.turns() * UNITS;       // accesses of a thread, at most
-    for (int g = w; g < chosen; g += part.warps)
-        for (int64_t q = lane; q < own; q += 32) {
-            const int64_t j = part.access(sh.chosen[g], q);
-            if (j >= 0) collect(sh, row, j, least);
-        }
+    collect(sh, row, part, chosen, least);
     __syncthreads();
     if (sh.count > CANDIDATES) {
+        // the k-th largest itself: the bits that were left out
+        for (; bit >= 0; --bit) {
+            const unsigned next = tau | 1u << bit;
+            if (__syncthreads_count(mine >= next) >= k) tau = next;
+        }
         __syncthreads();
         if (tid == 0) sh.count = 0;
         __syncthreads();
-        for (int g = w; g < chosen; g += part.warps)
-            for (int64_t q = lane; q < own; q += 32) {
-                const int64_t j = part.access(sh.chosen[g], q);
-                if (j >= 0) collect(sh, row, j, least + 1);
-            }
+        collect(sh, row, part, chosen, max(tau, 1u) + 1);
         __syncthreads();
         const int above = sh.count;
         __syncthreads();
         if (above > CANDIDATES) {
             // many far above the others, all in a few threads' hands: k rounds of the
             // largest one left
+            const int own = (int)part.turns();
             uint64_t last = ~0ull;
             for (int round = 0; round < k; ++round) {
                 uint64_t best = 0;
                 for (int g = w; g < chosen; g += part.warps)
-                    for (int64_t q = lane; q < own; q += 32) {
+                    for (int q = lane; q < own; q += 32) {
                         const int64_t j = part.access(sh.chosen[g], q);
                         if (j < 0) continue;
                         float f[W];
@@ -355,6 +390,10 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
     Part part{rank * share, 0, warps};
     part.units = max((int64_t)0, min(share, all_units - part.unit0));
     const float c = p.alpha * LOG2E;
+    // the target's logit, wanted at the end
+    const int target = tid == 0 && p.targets ? p.targets[r] : -1;
+    const bool has_target = target >= 0 && target < p.vocab;
+    const float target_logit = has_target ? to_f32(x[target]) : 0.0f;
     // logits up to here: c x is rounded by less than 1/16, so that a difference of two
     // equal ones, one of them rounded, stays small
     const float lim = fminf(1e30f, 1e6f / c);
@@ -364,7 +403,8 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
     // lose them on the way to the row's base.)
     const float low =
         to_f32(from_f32<T>(std::is_same_v<T, __half> ? fmaxf(-lim, -65504.0f) : -lim));
-    Largest<T> top(low);
+    Largest<T> top[UNITS] = {Largest<T>(low), Largest<T>(low), Largest<T>(low), Largest<T>(low)};
+    static_assert(UNITS == 4);
     Sums a{-INFINITY, 0.0f, 0.0f};
     float base = base_of(a.m, c, low);
     uint64_t s2 = pair(0.0f, 0.0f), u2 = s2;
@@ -385,8 +425,11 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
                     t + i < part.units ? j0 + 32 * i : (all_units + i) * 32 + lane);
         }
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) top.see(v[i]);
-        const float m = top.value();
+        for (int i = 0; i < UNITS; ++i) top[TOP ? i : 0].see(v[i]);
+        float m = top[0].value();
+        if (TOP)
+#pragma unroll
+            for (int i = 1; i < UNITS; ++i) m = fmaxf(m, top[i].value());
         if (m > a.m) {
             const float next = base_of(m, c, low);
             float s0, s1, u0, u1;
@@ -403,7 +446,7 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             float f[W];
-            top.floor(v[i], f);
+            top[0].floor(v[i], f);
 #pragma unroll
             for (int e = 0; e < W; e += 2) {
                 const uint64_t d2 = fma2(pair(f[e], f[e + 1]), c2, b2);
@@ -422,31 +465,28 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
         a.s = s0 + s1;
         a.u = u0 + u1;
     }
-    const unsigned mine = order_of(top.value());
-    {
-        // the warp's lanes to one base
-        const float m = warp_max(a.m);
-        rebase(a.s, a.u, base - base_of(m, c, low));
-        a.m = m;
-        a.s = warp_sum(a.s);
-        a.u = warp_sum(a.u);
-    }
+    a = join(a, c, low);
     if (lane == 0) sh.sums[w] = a;
     __syncthreads();
-    if (tid == 0) {
-        a = sh.sums[0];
-        for (int i = 1; i < warps; ++i) add(a, sh.sums[i], c, low);
-        sh.total = a;
+    if (w == 0) {
+        a = join(lane < warps ? sh.sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, c, low);
+        if (lane == 0) sh.total = a;
     }
-    if (TOP) choose(sh, row, part, mine, p.top_k);
+    if constexpr (TOP) {
+        unsigned group[UNITS];
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) group[i] = order_of(top[i].value());
+        choose(sh, row, part, group, p.top_k);
+    }
     __syncthreads();
     a = sh.total;
     if constexpr (SPLIT) {
-        // the first block joins the parts in order
+        // the first block joins the parts
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
         if (rank == 0) {
-            for (int i = 1; i < split; ++i) add(a, cluster.map_shared_rank(&sh, i)->total, c, low);
+            a = join(lane < split ? cluster.map_shared_rank(&sh, lane)->total
+                                  : Sums{-INFINITY, 0.0f, 0.0f}, c, low);
             if (TOP) {
                 const int n = split * p.top_k;      // at most one key per thread
                 uint64_t key = 0;
@@ -500,12 +540,8 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
     if (tid == 0) {
         if (p.lse) p.lse[r] = lse;
         if (p.entropy) p.entropy[r] = none ? 0.0f : LN2 * (log_s - a.u / a.s);
-        if (p.targets) {
-            const int t = p.targets[r];
-            float v = 0.0f;
-            if (t >= 0 && t < p.vocab) v = none ? -INFINITY : fmaf(p.alpha, to_f32(x[t]), -lse);
-            p.logprob[r] = v;
-        }
+        if (p.targets)
+            p.logprob[r] = !has_target ? 0.0f : none ? -INFINITY : fmaf(p.alpha, target_logit, -lse);
     }
     if (TOP && tid < p.top_k) {
         const uint64_t key = sh.best[tid];
@@ -525,9 +561,13 @@ cudaError_t launch_forward(const LogprobParams& p, int num_sms, cudaStream_t st)
     int split = 1;
     while (split < 8 && p.rows * split * 2 <= 2 * num_sms && units >= 64 * split) split *= 2;
     int64_t share = (units + split - 1) / split;
-    // A warp per 8 units, so that narrow rows leave room for other rows' blocks.
+    // Enough units per warp to carry a row's fixed cost (eight turns; two when the SMs are
+    // not full and the shortest call is wanted): fewer warps leave room for other rows.
+    // 4096 rows of 50,001 bf16: 95 us with 8 warps, 82 with 4; 16,384 rows of 1500 f32:
+    // 50 us with 2 warps, 39 with 1.
     int warps = LP_WARPS;
-    while (warps > 1 && share < 8 * warps / 2 && split == 1) warps /= 2;
+    const int64_t least = p.rows >= 4 * num_sms ? 8 * UNITS : 2 * UNITS;
+    while (warps > 1 && share < least * warps && split == 1) warps /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.rows * split));
     cfg.blockDim = dim3(32 * warps);

@@ -1,9 +1,16 @@
 // Layer norm y = (x - mean) * rstd * weight + bias over the rows of a matrix,
 // and its gradients with respect to x, weight and bias.
 //
-// Mean and deviations are binary32 sums; the deviations are taken from the
-// row's own mean in a second pass over the row, so no digits are lost to a
-// mean far from zero.
+// Mean and deviations are binary32 sums.  The deviations are taken from a mean
+// (the warp's, then corrected to the row's: for parts of n_w elements with means m_w,
+// sum (x - m)^2 = sum_w [sum (x - m_w)^2 + n_w (m_w - m)^2], all terms positive), so no
+// digits are lost to a mean far from zero.
+//
+// The kernels read rows in aligned 16-byte accesses wherever a row starts:
+// accesses are counted from the 16-byte boundary at or before the row's start, and
+// elements outside the row are left out.  A thread's rows lie a fixed stride apart
+// that keeps them at the same distance from such a boundary, so its columns,
+// and what it holds for them in registers, are the same for all of its rows.
 #include <algorithm>
 
 #include "spmm_internal.h"
@@ -13,30 +20,71 @@ namespace spmm {
 
 namespace {
 
-constexpr int NORM_THREADS = 256;
-constexpr int NORM_GRAD_THREADS = 512;   // the gradient's block: up to 128 registers a thread
+constexpr unsigned ALL = 0xffffffffu;
 
-// Sum over the block (every thread gets it); `s` holds one float per warp.
-template <int THREADS>
-__device__ __forceinline__ float block_sum(float x, float* s) {
-    x = warp_sum(x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-    __syncthreads();
-    float t = 0.0f;
+// ---- shared pieces ----------------------------------------------------------------
+
+// How a row lies on threads: `warps` warps of 32 lanes, or `lanes` < 32 lanes of one warp.
+struct Layout {
+    int lanes;
+    int warps;
+    int rows;                // rows of a block
+    int threads() const { return lanes * warps; }
+};
+
+__device__ __forceinline__ float lanes_sum(float x, int lanes) {
+    if (lanes == 32) return warp_sum(x);
+    for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
+    return x;
+}
+// Barrier of one row's warps (barrier 0 is the block's own).
+__device__ __forceinline__ void row_barrier(int row, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "r"(threads) : "memory");
+}
+
+// Elements [c, c + W) of a row of `dim`, those outside it 0.
+template <typename T, int W>
+__device__ __forceinline__ Vec<T, W> load_some(const T* row, int c, int dim) {
+    Vec<T, W> r;
+    if constexpr (W == 1) {
+        r.w = c >= 0 && c < dim ? row[c] : from_f32<T>(0.0f);
+    } else {
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) t += s[i];
-    return t;
+        for (int i = 0; i < Vec<T, W>::WORDS; ++i) r.w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (c + i < 0 || c + i >= dim) continue;
+            if constexpr (sizeof(T) == 4)
+                r.w[i] = reinterpret_cast<const uint32_t*>(row)[c + i];
+            else
+                r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c + i]
+                              << ((i & 1) * 16);
+        }
+    }
+    return r;
 }
-
-template <typename P>
-__device__ __forceinline__ float param(const void* p, int64_t i, float none) {
-    return p ? to_f32(static_cast<const P*>(p)[i]) : none;
-}
-
-// W parameters from column c, or the value `none` where there are none.
+// Parameters of columns [c, c + W), `none` where there are none.
 template <typename P, int W>
-__device__ __forceinline__ void params(const void* p, int64_t c, float none, float (&f)[W]) {
+__device__ __forceinline__ Vec<P, W> load_params(const void* p, int c, int dim, float none) {
+    if (!p) {
+        Vec<P, W> r;
+        const float f[2] = {none, none};
+#pragma unroll
+        for (int i = 0; i < Vec<P, W>::WORDS; ++i) {
+            if constexpr (sizeof(P) == 4) r.w[i] = __float_as_uint(none);
+            else r.w[i] = pack_word(f, P{});
+        }
+        return r;
+    }
+    const P* from = static_cast<const P*>(p);
+    if (c >= 0 && c + W <= dim && reinterpret_cast<uintptr_t>(from + c) % 16 == 0)
+        return load_vec<Cache::KEEP, P, W>(from + c);
+    return load_some<P, W>(from, c, dim);
+}
+
+// The same, whole and aligned.
+template <typename P, int W>
+__device__ __forceinline__ void vec_params(const void* p, int c, float none, float (&f)[W]) {
     if (p) {
         unpack(load_vec<Cache::KEEP, P, W>(static_cast<const P*>(p) + c), f);
     } else {
@@ -45,111 +93,202 @@ __device__ __forceinline__ void params(const void* p, int64_t c, float none, flo
     }
 }
 
-// Barrier of one row's warps (barrier 0 is the block's own).
-__device__ __forceinline__ void row_barrier(int row, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "r"(threads) : "memory");
+// A matrix's rows read in aligned accesses: one that reaches over the row's ends is
+// still a whole one where memory of the matrix lies there (another row, or the gap
+// between two), and is taken element by element at the matrix's own ends.
+template <typename T, int W>
+struct Rows {
+    const T* base;
+    int64_t ld;
+    const T* end;            // of the matrix
+    int dim;
+    __device__ Rows(const void* p, int64_t ld, int64_t rows, int64_t dim)
+        : base(static_cast<const T*>(p)), ld(ld), end(base + (rows - 1) * ld + dim), dim((int)dim) {}
+    __device__ const T* row(int64_t r) const { return base + r * ld; }
+    __device__ bool inside(const T* row, int c) const {
+        return (c >= 0 && c + W <= dim) || (row + c >= base && row + c + W <= end);
+    }
+    __device__ Vec<T, W> load(const T* row, int c) const {
+        return inside(row, c) ? load_vec<Cache::STREAM, T, W>(row + c) : load_some<T, W>(row, c, dim);
+    }
+    __device__ void copy(Vec<T, W>* to, const T* row, int c) const {
+        if (inside(row, c)) copy_async<T, W>(to, row + c);
+    }
+    // what copy() sent, or could not send
+    __device__ Vec<T, W> take(const Vec<T, W>* from, const T* row, int c) const {
+        return inside(row, c) ? *from : load_some<T, W>(row, c, dim);
+    }
+};
+template <typename T, int W>
+__device__ __forceinline__ void store_some(T* row, int c, int dim, const float (&f)[W]) {
+    if (c >= 0 && c + W <= dim) {
+        store_vec<Cache::STREAM, T, W>(row + c, f);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        if (c + i >= 0 && c + i < dim) row[c + i] = from_f32<T>(f[i]);
+}
+template <int W>
+__device__ __forceinline__ void clear_outside(int c, int dim, float (&f)[W]) {
+    if (c >= 0 && c + W <= dim) return;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        if (c + i < 0 || c + i >= dim) f[i] = 0.0f;
+}
+// Columns before the row's start that its first access covers.
+template <typename T, int W>
+__device__ __forceinline__ int lead_of(const T* row) {
+    return (int)(reinterpret_cast<uintptr_t>(row) % (W * sizeof(T)) / sizeof(T));
 }
 
-// Sum over a row's `warps` warps, in warp order; `s` has a slot for each.
-__device__ __forceinline__ float row_sum(float x, float* s, int row, int warps) {
-    x = warp_sum(x);
-    if (warps == 1) return x;
-    if ((threadIdx.x & 31) == 0) s[(threadIdx.x >> 5) % warps] = x;
-    row_barrier(row, warps * 32);
-    float t = 0.0f;
-    for (int i = 0; i < warps; ++i) t += s[i];
-    return t;
-}
+// ---- forward ------------------------------------------------------------------------
 
-// The row in registers: `warps` warps hold it in K accesses of W elements per
-// lane, so x is read once and the second pass over it costs no memory.  Several
-// narrow rows share a block.  With STAGES > 0 the row's warps walk the rows with
-// a fixed stride and keep STAGES - 1 rows ahead on their way to shared memory,
-// each lane's accesses in slots of its own.  The bound is HBM (read x, write y).
-template <typename T, typename P, int W, int K, int STAGES>
-__global__ __launch_bounds__(1024) void norm_rows(NormParams p, int warps, int nvec,
-                                                  int64_t stride) {
-    __shared__ float s[2][32];
-    extern __shared__ __align__(16) unsigned char ring_bytes[];
-    const int threads = warps * 32;
+// How a row meets its threads' accesses: ALL: every lane's are whole and in the row, and
+// there are a weight and a bias; WHOLE: whole, some lanes have fewer; EDGES: any width,
+// any start.
+enum class Fit { ALL, WHOLE, EDGES };
+
+// A row in registers, K accesses of W elements per lane: read once, one exchange
+// between its warps.  The bound is HBM (read x, write y) as long as an element costs
+// few instructions: 65,521 f16 rows of 8192 took 476 us at 27 per element and take 366
+// at 18, two at a time and without a branch.  Rows with edges walk the matrix with a
+// fixed grid and keep the parameters in shared memory in binary32, (weight, bias)
+// of column c at [c mod W][c / W]: wherever a row starts, a warp reads neighbours.
+// The others have a block of threads each and read the parameters from L1.
+template <typename T, typename P, int W, int K, Fit FIT>
+__global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_t stride,
+                                                  int pitch) {
+    constexpr bool EDGES = FIT == Fit::EDGES;
+    __shared__ float4 slots[2][32];
+    extern __shared__ __align__(16) float2 params[];     // [W][pitch]
+    const int threads = l.lanes * l.warps;
     const int in_block = threadIdx.x / threads, tid = threadIdx.x % threads;
-    const T* xs = static_cast<const T*>(p.x);
-    int64_t r = (int64_t)blockIdx.x * (blockDim.x / threads) + in_block;
-    Vec<T, W>* ring = reinterpret_cast<Vec<T, W>*>(ring_bytes) + threadIdx.x;
-    auto copy = [&](int64_t row, int stage) {
-        if constexpr (STAGES > 0) {
-            if (row < p.rows)
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (k * threads + tid < nvec)
-                        copy_async<T, W>(ring + (stage * K + k) * blockDim.x,
-                                         xs + row * p.ldx + (int64_t)(k * threads + tid) * W);
-            copies_issued();
+    const int lane = threadIdx.x & 31;
+    const Rows<T, W> x(p.x, p.ldx, p.rows, p.dim);
+    const int dim = (int)p.dim;
+    const int step = threads * W;                // columns from one access to the next
+    int64_t r = (int64_t)blockIdx.x * l.rows + in_block;
+    int64_t first = r - lane / l.lanes;          // the warp's first row: all lanes stay together
+    if constexpr (EDGES) {
+        for (int c = threadIdx.x; c < dim; c += blockDim.x) {
+            params[(c % W) * pitch + c / W] =
+                make_float2(p.weight ? to_f32(static_cast<const P*>(p.weight)[c]) : 1.0f,
+                            p.bias ? to_f32(static_cast<const P*>(p.bias)[c]) : 0.0f);
         }
-    };
-    for (int i = 0; i < STAGES - 1; ++i) copy(r + i * stride, i);
-    int stage = 0;
-    for (; r < p.rows; r += stride) {
+        __syncthreads();
+    }
+    // the rows' first accesses begin `lead` columns before them; element i of access j is
+    // column j W + i - lead
+    const int lead = EDGES ? lead_of<T, W>(x.row(r)) : 0;
+    int param_at[EDGES ? W : 1];
+#pragma unroll
+    for (int i = 0; i < (EDGES ? W : 0); ++i) {
+        const int e = i - lead + W;              // > 0
+        param_at[i] = e % W * pitch + e / W - 1 + tid;
+    }
+    const float per_dim = 1.0f / (float)dim;
+    int turn = 0;
+    for (; first < p.rows; first += stride, r += stride) {
+        const T* row = x.row(r);
+        const int c0 = tid * W - lead;
+        const bool live = FIT == Fit::ALL || r < p.rows;
         Vec<T, W> held[K];
-        if constexpr (STAGES > 0) {
-            copies_wait<(STAGES > 1 ? STAGES - 2 : 0)>();
-#pragma unroll
-            for (int k = 0; k < K; ++k) held[k] = ring[(stage * K + k) * blockDim.x];
-            copy(r + (STAGES - 1) * stride, stage == 0 ? STAGES - 1 : stage - 1);
-            stage = stage == STAGES - 1 ? 0 : stage + 1;
-        } else {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (k * threads + tid < nvec)
-                    held[k] = load_vec<Cache::STREAM, T, W>(xs + r * p.ldx +
-                                                            (int64_t)(k * threads + tid) * W);
-        }
-        // one access per lane is the case of few rows, where latency counts: the
-        // parameters are on their way during the sums
-        float w0[W], b0[W];
-        if constexpr (K == 1)
-            if (tid < nvec) {
-                params<P, W>(p.weight, tid * W, 1.0f, w0);
-                params<P, W>(p.bias, tid * W, 0.0f, b0);
-            }
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (k * threads + tid < nvec) {
-                float f[W];
-                unpack(held[k], f);
-#pragma unroll
-                for (int i = 0; i < W; ++i) sum += f[i];
-            }
-        float* slot = s[0] + in_block * warps;
-        const float mean = row_sum(sum, slot, in_block, warps) / (float)p.dim;
-        sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (k * threads + tid < nvec) {
-                float f[W];
-                unpack(held[k], f);
-#pragma unroll
-                for (int i = 0; i < W; ++i) sum += (f[i] - mean) * (f[i] - mean);
-            }
-        slot = s[1] + in_block * warps;
-        const float var = row_sum(sum, slot, in_block, warps) / (float)p.dim;
-        const float rstd = 1.0f / sqrtf(var + p.eps);
-        T* y = static_cast<T*>(p.y) + r * p.ldy;
+        int own = 0;                             // elements of the row in this lane
+        auto in = [&](int k) { return FIT == Fit::ALL || (live && c0 + k * step < dim); };
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int at = k * threads + tid;
-            if (at >= nvec) continue;
-            float f[W], w[W], b[W];
+            const int c = c0 + k * step;
+            if (!in(k)) continue;
+            held[k] = EDGES ? x.load(row, c) : load_vec<Cache::STREAM, T, W>(row + c);
+            own += EDGES ? min(c + W, dim) - max(c, 0) : W;
+        }
+        uint64_t sums = pair(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (!in(k)) continue;
+            float f[W];
             unpack(held[k], f);
-            if constexpr (K > 1) {
-                params<P, W>(p.weight, at * W, 1.0f, w);
-                params<P, W>(p.bias, at * W, 0.0f, b);
+            if (EDGES) clear_outside(c0 + k * step, dim, f);
+#pragma unroll
+            for (int i = 0; i < W; i += 2) sums = add2(sums, pair(f[i], f[i + 1]));
+        }
+        float lo, hi;
+        halves(sums, lo, hi);
+        float sum = lanes_sum(lo + hi, l.lanes);
+        // any number near the mean of the warp's part will do
+        const float count = FIT == Fit::ALL ? (float)(l.lanes * W * K)
+                                            : lanes_sum((float)own, l.lanes);
+        float mean = count > 0.0f ? __fdividef(sum, count) : 0.0f;
+        sums = pair(0.0f, 0.0f);
+        uint64_t m2 = pair(-mean, -mean);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (!in(k)) continue;
+            float f[W];
+            unpack(held[k], f);
+            if (EDGES) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) f[i] -= mean;
+                clear_outside(c0 + k * step, dim, f);
             }
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                f[i] = (f[i] - mean) * rstd * (K == 1 ? w0[i] : w[i]) + (K == 1 ? b0[i] : b[i]);
-            store_vec<Cache::STREAM, T, W>(y + (int64_t)at * W, f);
+            for (int i = 0; i < W; i += 2) {
+                uint64_t d = pair(f[i], f[i + 1]);
+                if (!EDGES) d = add2(d, m2);
+                sums = fma2(d, d, sums);
+            }
+        }
+        halves(sums, lo, hi);
+        float squares = lanes_sum(lo + hi, l.lanes);
+        if (l.warps > 1) {
+            // two sets of slots in turn: one barrier per row keeps them apart
+            float4* s = slots[turn] + in_block * l.warps;
+            turn ^= 1;
+            if (lane == 0) s[tid >> 5] = make_float4(sum, mean, squares, count);
+            row_barrier(in_block, threads);
+            sum = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < l.warps; ++i) sum += s[i].x;
+            mean = sum * per_dim;
+            squares = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < l.warps; ++i)
+                squares += s[i].z + s[i].w * (s[i].y - mean) * (s[i].y - mean);
+        }
+        if (!live) continue;                     // narrow rows: a warp holds several
+        const float rstd = rsqrtf(squares * per_dim + p.eps);
+        T* y = static_cast<T*>(p.y) + r * p.ldy;
+        const uint64_t r2 = pair(rstd, rstd);
+        m2 = pair(-mean, -mean);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = c0 + k * step;
+            if (!in(k)) continue;
+            float f[W], w[W], b[W];
+            unpack(held[k], f);
+            if constexpr (EDGES) {
+                // outside the row whatever lies there
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const float2 wb = params[param_at[i] + k * threads];
+                    w[i] = wb.x;
+                    b[i] = wb.y;
+                }
+            } else if constexpr (FIT == Fit::ALL) {
+                unpack(load_vec<Cache::KEEP, P, W>(static_cast<const P*>(p.weight) + c), w);
+                unpack(load_vec<Cache::KEEP, P, W>(static_cast<const P*>(p.bias) + c), b);
+            } else {
+                vec_params<P, W>(p.weight, c, 1.0f, w);
+                vec_params<P, W>(p.bias, c, 0.0f, b);
+            }
+#pragma unroll
+            for (int i = 0; i < W; i += 2) {
+                const uint64_t d = mul2(add2(pair(f[i], f[i + 1]), m2), r2);
+                halves(fma2(d, pair(w[i], w[i + 1]), pair(b[i], b[i + 1])), f[i], f[i + 1]);
+            }
+            if (EDGES) store_some<T, W>(y, c, dim, f);
+            else store_vec<Cache::STREAM, T, W>(y + c, f);
         }
         if (tid == 0) {
             if (p.mean) p.mean[r] = mean;
@@ -158,24 +297,43 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, int warps, int n
     }
 }
 
-// Any width and alignment: a block per row, the row read again for each pass.
+constexpr int ANY_THREADS = 256;
+
+// Sum over the block (every thread gets it); `s` holds one float per warp.
+__device__ __forceinline__ float block_sum(float x, float* s) {
+    x = warp_sum(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ANY_THREADS / 32; ++i) t += s[i];
+    return t;
+}
+template <typename P>
+__device__ __forceinline__ float param(const void* p, int64_t i, float none) {
+    return p ? to_f32(static_cast<const P*>(p)[i]) : none;
+}
+
+// Rows too wide for registers, or x and y that lie differently against 16-byte
+// boundaries: a block per row, element by element, the row read again for each pass.
 template <typename T, typename P>
-__global__ __launch_bounds__(NORM_THREADS) void norm_any(NormParams p) {
-    __shared__ float s[NORM_THREADS / 32];
+__global__ __launch_bounds__(ANY_THREADS) void norm_any(NormParams p) {
+    __shared__ float s[ANY_THREADS / 32];
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const T* x = static_cast<const T*>(p.x) + r * p.ldx;
         T* y = static_cast<T*>(p.y) + r * p.ldy;
         float sum = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.dim; c += NORM_THREADS) sum += to_f32(x[c]);
-        const float mean = block_sum<NORM_THREADS>(sum, s) / (float)p.dim;
+        for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) sum += to_f32(x[c]);
+        const float mean = block_sum(sum, s) / (float)p.dim;
         sum = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.dim; c += NORM_THREADS) {
+        for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) {
             const float d = to_f32(x[c]) - mean;
             sum += d * d;
         }
-        const float var = block_sum<NORM_THREADS>(sum, s) / (float)p.dim;
-        const float rstd = 1.0f / sqrtf(var + p.eps);
-        for (int64_t c = threadIdx.x; c < p.dim; c += NORM_THREADS)
+        const float var = block_sum(sum, s) / (float)p.dim;
+        const float rstd = rsqrtf(var + p.eps);
+        for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS)
             y[c] = from_f32<T>((to_f32(x[c]) - mean) * rstd * param<P>(p.weight, c, 1.0f) +
                                param<P>(p.bias, c, 0.0f));
         if (threadIdx.x == 0) {
@@ -185,195 +343,229 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_any(NormParams p) {
     }
 }
 
-// dx, and this block's share of dweight and dbias, in one pass over dy and x: a
-// row's `warps` warps hold it in registers, walk the rows with a fixed stride, and keep their
-// columns' sums of dy * xhat and dy in registers to the end.  The rows ahead are
-// on their way to shared memory, each lane's accesses in slots of its own
-// (single 16-bit elements cannot be copied so: the next row waits in registers).
-// The bound is HBM (read dy and x, write dx).  part: [slices][2][dim].
-// Stages of the ring: what 512 threads can have of the 227 KB, four at most.
-template <typename T, int W, int K>
-constexpr int GRAD_STAGES = sizeof(T) * W * K > 32 ? 3 : 4;
-template <typename T, typename P, int W, int K>
-__global__ __launch_bounds__(NORM_GRAD_THREADS) void norm_grad_rows(NormGradParams p, int warps,
-                                                                    int nvec, int slices) {
-    __shared__ float s[2][2][32];
-    const int threads = warps * 32;
-    const int in_block = threadIdx.x / threads, tid = threadIdx.x % threads;
-    const int slice = blockIdx.x * (blockDim.x / threads) + in_block;
-    if (slice >= slices) return;
-    const T* xs = static_cast<const T*>(p.x);
-    const T* dys = static_cast<const T*>(p.dy);
-    const bool sums = p.dweight || p.dbias;
-    // 16 elements a lane leave no registers for the weights in binary32 (W = 4) and
-    // for single accesses (W = 1): those read them again for each row, from L1
-    constexpr bool HOLD = W * K < 16 || W == 8;
-    constexpr bool RING = can_copy_async<T, W>;
-    constexpr int STAGES = GRAD_STAGES<T, W, K>;
+// ---- gradient -----------------------------------------------------------------------
+
+constexpr int GRAD_THREADS = 512;    // a row's threads, at most; up to 128 registers each
+constexpr int GRAD_COLUMNS = GRAD_THREADS * 16;
+// Stages of the ring: what GRAD_THREADS threads can have of the 227 KB, four at most.
+template <typename T>
+constexpr int GRAD_STAGES = sizeof(T) == 4 ? 3 : 4;
+
+// dx, and this group's share of dweight and dbias, in one pass over dy and x: a row's
+// threads walk the rows with a fixed stride, the rows ahead on their way to shared
+// memory (each lane's accesses in slots of its own), and keep their columns' sums of
+// dy * xhat and dy in registers to the end.  GIVEN: rows of more than GRAD_COLUMNS
+// columns, in tiles of as many (blockIdx.y); the row's two means come from
+// grad_means and nothing is exchanged.  The bound is HBM (read dy and x, write dx).
+// part: [slices, or blocks of narrow rows][2][dim].
+template <typename T, typename P, int W, int K, bool GIVEN>
+__global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p, Layout l,
+                                                               int slices) {
+    constexpr int STAGES = GRAD_STAGES<T>;
+    __shared__ float2 slots[2][32];
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     Vec<T, W>* ring = reinterpret_cast<Vec<T, W>*>(ring_bytes) + threadIdx.x;
-    Vec<T, W> x[K], dy[K];
-    float weight[HOLD ? K : 1][W], dw[K][W], db[K][W];
-    // sends for row r: to a stage of the ring, or to the registers
-    auto fetch = [&](int64_t r, int stage) {
-        if (r < p.rows)
+    const int threads = l.lanes * l.warps;
+    const int in_block = threadIdx.x / threads, tid = threadIdx.x % threads;
+    const int lane = threadIdx.x & 31;
+    const Rows<T, W> x(p.x, p.ldx, p.rows, p.dim), dy(p.dy, p.ld_dy, p.rows, p.dim);
+    const int dim = (int)p.dim;
+    const int slice = blockIdx.x * l.rows + in_block;
+    int64_t r = slice, first = r - lane / l.lanes;
+    // the tile's accesses follow the ones of the tiles before, so none is in two tiles
+    const int c0 = tid * W - lead_of<T, W>(x.row(r)) + (GIVEN ? (int)blockIdx.y * GRAD_COLUMNS : 0);
+    const int step = threads * W;
+    auto fetch = [&](int64_t row, int stage) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int at = k * threads + tid;
-                if (at >= nvec) continue;
-                const T* xr = xs + r * p.ldx + (int64_t)at * W;
-                const T* dyr = dys + r * p.ld_dy + (int64_t)at * W;
-                if constexpr (RING) {
-                    copy_async<T, W>(ring + (stage * 2 * K + k) * blockDim.x, xr);
-                    copy_async<T, W>(ring + (stage * 2 * K + K + k) * blockDim.x, dyr);
-                } else {
-                    x[k] = load_vec<Cache::STREAM, T, W>(xr);
-                    dy[k] = load_vec<Cache::STREAM, T, W>(dyr);
-                }
+        for (int k = 0; k < K; ++k)
+            if (row < p.rows && c0 + k * step < dim) {
+                x.copy(ring + (stage * 2 * K + k) * blockDim.x, x.row(row), c0 + k * step);
+                dy.copy(ring + (stage * 2 * K + K + k) * blockDim.x, dy.row(row), c0 + k * step);
             }
-        if constexpr (RING) copies_issued();
+        copies_issued();
     };
-    if constexpr (RING)
-        for (int i = 0; i < STAGES - 1; ++i) fetch(slice + (int64_t)i * slices, i);
-    else
-        fetch(slice, 0);
+    // slices beyond the grid's last row group have no rows (slice >= slices)
+    const int64_t rows = slice - lane / l.lanes < slices ? p.rows : 0;
+    if (rows > 0)
+        for (int i = 0; i < STAGES - 1; ++i) fetch(r + (int64_t)i * slices, i);
+    Vec<P, W> w[K];
+    uint64_t dw[K][W / 2], db[K][W / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) dw[k][i] = db[k][i] = 0.0f;
-        if (HOLD && k * threads + tid < nvec)
-            params<P, W>(p.weight, (int64_t)(k * threads + tid) * W, 1.0f, weight[HOLD ? k : 0]);
+        for (int i = 0; i < W / 2; ++i) dw[k][i] = db[k][i] = pair(0.0f, 0.0f);
+        if (c0 + k * step < dim) w[k] = load_params<P, W>(p.weight, c0 + k * step, dim, 1.0f);
     }
+    const float per_dim = 1.0f / (float)dim;
     int turn = 0, stage = 0;
-    for (int64_t r = slice; r < p.rows; r += slices) {
-        if constexpr (RING) {
-            copies_wait<STAGES - 2>();
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                x[k] = ring[(stage * 2 * K + k) * blockDim.x];
-                dy[k] = ring[(stage * 2 * K + K + k) * blockDim.x];
-            }
-            fetch(r + (int64_t)(STAGES - 1) * slices, stage == 0 ? STAGES - 1 : stage - 1);
-            stage = stage == STAGES - 1 ? 0 : stage + 1;
-        }
-        const float mean = p.mean[r], rstd = p.rstd[r];
-        float xh[K][W], g[K][W];
-        float a = 0.0f, b = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (k * threads + tid < nvec) {
-                unpack(x[k], xh[k]);
-                unpack(dy[k], g[k]);
-                float (&wk)[W] = weight[HOLD ? k : 0];
-                if (!HOLD) params<P, W>(p.weight, (int64_t)(k * threads + tid) * W, 1.0f, wk);
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    xh[k][i] = (xh[k][i] - mean) * rstd;
-                    dw[k][i] += g[k][i] * xh[k][i];
-                    db[k][i] += g[k][i];
-                    g[k][i] *= wk[i];
-                    a += g[k][i];
-                    b += g[k][i] * xh[k][i];
-                }
-            }
-        if constexpr (!RING) fetch(r + slices, 0);
-        a = warp_sum(a);
-        b = warp_sum(b);
-        if (warps > 1) {
-            // two sets of slots in turn: one barrier per row keeps them apart
-            float* sa = s[turn][0] + in_block * warps;
-            float* sb = s[turn][1] + in_block * warps;
-            turn ^= 1;
-            if ((threadIdx.x & 31) == 0) {
-                sa[tid >> 5] = a;
-                sb[tid >> 5] = b;
-            }
-            row_barrier(in_block, threads);
-            a = b = 0.0f;
-            for (int i = 0; i < warps; ++i) {
-                a += sa[i];
-                b += sb[i];
-            }
-        }
-        a /= (float)p.dim;
-        b /= (float)p.dim;
-        T* dx = static_cast<T*>(p.dx) + r * p.ld_dx;
+    // the next row's statistics are on their way during this one's sums
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    float2 next_ab{};
+    auto statistics = [&](int64_t row) {
+        if (row >= rows || slice >= slices) return;
+        next_mean = p.mean[row];
+        next_rstd = p.rstd[row];
+        if (GIVEN) next_ab = reinterpret_cast<const float2*>(p.means)[row];
+    };
+    statistics(r);
+    for (; first < rows; first += slices, r += slices) {
+        const bool live = r < rows && slice < slices;
+        const float mean = next_mean, rstd = next_rstd;
+        const float2 ab = next_ab;
+        statistics(r + slices);
+        copies_wait<STAGES - 2>();
+        uint64_t xh[K][W / 2], g[K][W / 2];
+        uint64_t a2 = pair(0.0f, 0.0f), b2 = a2;
+        const uint64_t m2 = pair(-mean, -mean), r2 = pair(rstd, rstd);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int at = k * threads + tid;
-            if (at >= nvec) continue;
+            const int c = c0 + k * step;
+            if (!live || c >= dim) continue;
+            float xf[W], gf[W], wf[W];
+            unpack(x.take(ring + (stage * 2 * K + k) * blockDim.x, x.row(r), c), xf);
+            unpack(dy.take(ring + (stage * 2 * K + K + k) * blockDim.x, dy.row(r), c), gf);
+            clear_outside(c, dim, gf);
+            clear_outside(c, dim, xf);
+            unpack(w[k], wf);
 #pragma unroll
-            for (int i = 0; i < W; ++i) g[k][i] = rstd * (g[k][i] - a - xh[k][i] * b);
-            store_vec<Cache::STREAM, T, W>(dx + (int64_t)at * W, g[k]);
+            for (int i = 0; i < W / 2; ++i) {
+                const uint64_t d = pair(gf[2 * i], gf[2 * i + 1]);
+                xh[k][i] = mul2(add2(pair(xf[2 * i], xf[2 * i + 1]), m2), r2);
+                dw[k][i] = fma2(d, xh[k][i], dw[k][i]);
+                db[k][i] = add2(db[k][i], d);
+                g[k][i] = mul2(d, pair(wf[2 * i], wf[2 * i + 1]));
+                if (!GIVEN) {
+                    a2 = add2(a2, g[k][i]);
+                    b2 = fma2(g[k][i], xh[k][i], b2);
+                }
+            }
+        }
+        fetch(r + (int64_t)(STAGES - 1) * slices, stage == 0 ? STAGES - 1 : stage - 1);
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
+        float a, b;
+        if constexpr (GIVEN) {
+            a = ab.x;
+            b = ab.y;
+        } else {
+            float lo, hi;
+            halves(a2, lo, hi);
+            a = lanes_sum(lo + hi, l.lanes);
+            halves(b2, lo, hi);
+            b = lanes_sum(lo + hi, l.lanes);
+            if (l.warps > 1) {
+                // two sets of slots in turn: one barrier per row keeps them apart
+                float2* s = slots[turn] + in_block * l.warps;
+                turn ^= 1;
+                if (lane == 0) s[tid >> 5] = make_float2(a, b);
+                row_barrier(in_block, threads);
+                a = b = 0.0f;
+#pragma unroll 8
+                for (int i = 0; i < l.warps; ++i) {
+                    a += s[i].x;
+                    b += s[i].y;
+                }
+            }
+            a *= per_dim;
+            b *= per_dim;
+        }
+        if (!live) continue;
+        T* dx = static_cast<T*>(p.dx) + r * p.ld_dx;
+        const uint64_t na = pair(-a, -a), nb = pair(-b, -b);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = c0 + k * step;
+            if (c >= dim) continue;
+            float f[W];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i)
+                halves(mul2(r2, fma2(nb, xh[k][i], add2(g[k][i], na))), f[2 * i], f[2 * i + 1]);
+            store_some<T, W>(dx, c, dim, f);
         }
     }
     allow_successor();
-    if (!sums) return;
-    float* part = p.part + (int64_t)slice * 2 * p.dim;
+    if (!p.part) return;
+    // one part per row group; narrow rows, many to a block, are first added up there
+    const bool narrow = l.lanes < 32;
+    float* part = p.part + (int64_t)(narrow ? blockIdx.x : slice) * 2 * p.dim;
+    if (narrow) {
+        copies_wait<0>();
+        __syncthreads();
+        part = reinterpret_cast<float*>(ring_bytes);
+        for (int i = threadIdx.x; i < 2 * dim; i += blockDim.x) part[i] = 0.0f;
+    }
+    for (int turn_of = 0; turn_of < (narrow ? l.rows : 1); ++turn_of) {
+        if (narrow) __syncthreads();
+        if (slice >= slices || (narrow && turn_of != in_block)) continue;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int at = k * threads + tid;
-        if (at >= nvec) continue;
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            part[(int64_t)at * W + i] = dw[k][i];
-            part[p.dim + (int64_t)at * W + i] = db[k][i];
-        }
+            for (int i = 0; i < W / 2; ++i) {
+                const int c = c0 + k * step + 2 * i;
+                float wf[2], bf[2];
+                halves(dw[k][i], wf[0], wf[1]);
+                halves(db[k][i], bf[0], bf[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (c + e < 0 || c + e >= dim) continue;
+                    part[c + e] = narrow ? part[c + e] + wf[e] : wf[e];
+                    part[dim + c + e] = narrow ? part[dim + c + e] + bf[e] : bf[e];
+                }
+            }
+    }
+    if (narrow) {
+        __syncthreads();
+        float* to = p.part + (int64_t)blockIdx.x * 2 * p.dim;
+        for (int i = threadIdx.x; i < 2 * dim; i += blockDim.x) to[i] = part[i];
     }
 }
 
-// Any width and alignment: dx, a block per row.
+// The two means of each row, element by element: a block per row.
 template <typename T, typename P>
-__global__ __launch_bounds__(NORM_THREADS) void norm_dx_any(NormGradParams p) {
-    __shared__ float s[NORM_THREADS / 32];
+__global__ __launch_bounds__(ANY_THREADS) void grad_means(NormGradParams p) {
+    __shared__ float s[ANY_THREADS / 32];
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const T* x = static_cast<const T*>(p.x) + r * p.ldx;
         const T* dy = static_cast<const T*>(p.dy) + r * p.ld_dy;
-        T* dx = static_cast<T*>(p.dx) + r * p.ld_dx;
         const float mean = p.mean[r], rstd = p.rstd[r];
         float a = 0.0f, b = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.dim; c += NORM_THREADS) {
+#pragma unroll 4
+        for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) {
             const float g = to_f32(dy[c]) * param<P>(p.weight, c, 1.0f);
             a += g;
             b += g * ((to_f32(x[c]) - mean) * rstd);
         }
-        a = block_sum<NORM_THREADS>(a, s) / (float)p.dim;
-        b = block_sum<NORM_THREADS>(b, s) / (float)p.dim;
-        for (int64_t c = threadIdx.x; c < p.dim; c += NORM_THREADS) {
-            const float g = to_f32(dy[c]) * param<P>(p.weight, c, 1.0f);
-            dx[c] = from_f32<T>(rstd * (g - a - (to_f32(x[c]) - mean) * rstd * b));
-        }
+        a = block_sum(a, s) / (float)p.dim;
+        b = block_sum(b, s) / (float)p.dim;
+        if (threadIdx.x == 0) reinterpret_cast<float2*>(p.means)[r] = make_float2(a, b);
     }
 }
 
-// Column sums of dy * xhat and dy over a slice of the rows: a warp per row of
-// 32 columns, blocks (column tile, slice).  part: [slices][2][dim].
+// Where x, dy and dx lie differently against 16-byte boundaries: element by element,
+// a thread per column and slice of the rows, the row's means from grad_means.
 constexpr int SLICE_ROWS = 256;
-template <typename T>
-__global__ __launch_bounds__(256) void norm_dw_any(NormGradParams p) {
-    __shared__ float s[2][8][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+template <typename T, typename P>
+__global__ __launch_bounds__(ANY_THREADS) void norm_grad_any(NormGradParams p) {
+    const int64_t c = (int64_t)blockIdx.x * ANY_THREADS + threadIdx.x;
+    if (c >= p.dim) return;
+    const float w = param<P>(p.weight, c, 1.0f);
+    float dw = 0.0f, db = 0.0f;
     const int64_t r0 = (int64_t)blockIdx.y * SLICE_ROWS;
     const int64_t r1 = min(r0 + SLICE_ROWS, p.rows);
-    float dw = 0.0f, db = 0.0f;
-    if (c < p.dim) {
-        for (int64_t r = r0 + w; r < r1; r += 8) {
-            const float g = to_f32(static_cast<const T*>(p.dy)[r * p.ld_dy + c]);
-            const float x = to_f32(static_cast<const T*>(p.x)[r * p.ldx + c]);
-            dw += g * ((x - p.mean[r]) * p.rstd[r]);
-            db += g;
-        }
+#pragma unroll 4
+    for (int64_t r = r0; r < r1; ++r) {
+        const float g = to_f32(static_cast<const T*>(p.dy)[r * p.ld_dy + c]);
+        const float x = to_f32(static_cast<const T*>(p.x)[r * p.ldx + c]);
+        const float rstd = p.rstd[r];
+        const float xhat = (x - p.mean[r]) * rstd;
+        const float2 ab = reinterpret_cast<const float2*>(p.means)[r];
+        dw += g * xhat;
+        db += g;
+        static_cast<T*>(p.dx)[r * p.ld_dx + c] =
+            from_f32<T>(rstd * (g * w - ab.x - xhat * ab.y));
     }
-    s[0][w][lane] = dw;
-    s[1][w][lane] = db;
-    __syncthreads();
-    if (w < 2 && c < p.dim) {
-        float t = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t += s[w][i][lane];
-        p.part[((int64_t)blockIdx.y * 2 + w) * p.dim + c] = t;
-    }
+    if (!p.part) return;
+    p.part[(int64_t)blockIdx.y * 2 * p.dim + c] = dw;
+    p.part[((int64_t)blockIdx.y * 2 + 1) * p.dim + c] = db;
 }
 
 // dweight and dbias from the slices' partial sums: a block takes 32 columns, each
@@ -404,21 +596,35 @@ __global__ __launch_bounds__(32 * JOIN_WARPS) void norm_dw_join(NormGradParams p
     out[c] = from_f32<P>(t);
 }
 
-int64_t slices_any(int64_t rows) { return (rows + SLICE_ROWS - 1) / SLICE_ROWS; }
+// ---- launch -----------------------------------------------------------------------------
 
-// Warps that hold a row of nvec accesses, K per lane.
-int warps_for(int64_t nvec, int K) {
-    int warps = 1;
-    while ((int64_t)warps * 32 * K < nvec) warps *= 2;
-    return warps;
+// The layout of rows of `columns` columns, K accesses of W elements per lane, in
+// blocks of at least `least` threads.
+Layout layout_of(int64_t columns, int W, int K, int least) {
+    const int64_t lanes = (columns + (int64_t)W * K - 1) / ((int64_t)W * K);
+    Layout l{1, 1, 1};
+    while (l.lanes < 32 && l.lanes < lanes) l.lanes *= 2;
+    while ((int64_t)l.lanes * l.warps < lanes) l.warps *= 2;
+    l.rows = std::max(1, least / l.threads());
+    return l;
 }
 
-// Slices of the register kernel's grid: one row at a time each, as many as the
-// SMs hold (`sm_warps` warps each, by the kernel's registers).
-int64_t slices_rows(int64_t rows, int warps, int num_sms, int sm_warps) {
-    return std::min<int64_t>(rows, (int64_t)num_sms * sm_warps / warps);
+// A row of `dim` columns covers up to W - 1 more where it starts between boundaries.
+bool off_boundary(const void* p, int64_t ld, size_t es) {
+    return reinterpret_cast<uintptr_t>(p) % 16 != 0 || ld * (int64_t)es % 16 != 0;
 }
-constexpr int SM_WARPS_MOST = 32;    // 64 registers a thread: up to 4 elements per lane
+// Each row of one at the same distance from a 16-byte boundary as in the other.
+bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, size_t es) {
+    return (reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b)) % 16 == 0 &&
+           (lda - ldb) * (int64_t)es % 16 == 0;
+}
+// Blocks of `rows` rows for a grid of at most `most`; a grid that does not cover the rows
+// at once keeps its stride a multiple of W rows.
+int64_t blocks_of(int64_t total, int rows, int64_t most, int W) {
+    const int64_t blocks = (total + rows - 1) / rows;
+    if (blocks <= most) return blocks;
+    return rows % W == 0 ? most : std::max<int64_t>(W, most / W * W);
+}
 
 template <typename... KArgs>
 cudaError_t allow_shared(void (*kernel)(KArgs...), size_t bytes) {
@@ -427,119 +633,138 @@ cudaError_t allow_shared(void (*kernel)(KArgs...), size_t bytes) {
                                                  (int)bytes);
 }
 
-template <typename T, typename P, int W, int K, int STAGES>
-cudaError_t norm_launch(const NormParams& p, int num_sms, cudaStream_t st) {
-    const int nvec = (int)(p.dim / W);
-    const int warps = warps_for(nvec, K);
-    const int rows = std::max(1, 8 / warps);          // at least 256 threads
-    int64_t blocks = (p.rows + rows - 1) / rows;
-    // with a ring: as many blocks as the SMs hold at 64 registers a thread
-    if (STAGES > 0) blocks = std::min<int64_t>(blocks, (int64_t)num_sms * (32 / (rows * warps)));
-    const size_t shared = (size_t)STAGES * K * rows * warps * 32 * sizeof(Vec<T, W>);
-    auto kernel = norm_rows<T, P, W, K, STAGES>;
+template <typename T, typename P, int W, int K, bool WHOLE>
+cudaError_t norm_launch(const NormParams& p, int64_t columns, int num_sms, cudaStream_t st) {
+    const Layout l = layout_of(columns, W, K, 256);
+    const int threads = l.threads() * l.rows;
+    int64_t blocks = (p.rows + l.rows - 1) / l.rows;
+    int pitch = 0;
+    auto kernel = norm_rows<T, P, W, K, WHOLE ? Fit::WHOLE : Fit::EDGES>;
+    if constexpr (!WHOLE) {
+        blocks = blocks_of(p.rows, l.rows, (int64_t)num_sms * std::max(1, 1024 / threads), W);
+        pitch = ((int)(p.dim / W) + 2) | 1;
+    } else if (p.dim == (int64_t)l.threads() * W * K && p.rows % l.rows == 0 && p.weight &&
+               p.bias) {
+        kernel = norm_rows<T, P, W, K, Fit::ALL>;
+    }
+    const size_t shared = (size_t)W * pitch * sizeof(float2);
     cudaError_t e = allow_shared(kernel, shared);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)blocks, rows * warps * 32, shared, st>>>(p, warps, nvec, blocks * rows);
+    kernel<<<(unsigned)blocks, threads, shared, st>>>(p, l, blocks * l.rows, pitch);
     return cudaGetLastError();
 }
 
-template <typename T, typename P, int W, int K>
-cudaError_t norm_grad_launch(const NormGradParams& p, int num_sms, cudaStream_t st, int* slices) {
-    const int nvec = (int)(p.dim / W);
-    const int warps = warps_for(nvec, K);
-    const int rows = std::max(1, 4 / warps);          // at least 128 threads
-    constexpr int SM_WARPS = W * K <= 4 ? SM_WARPS_MOST : SM_WARPS_MOST / 2;
-    *slices = (int)slices_rows(p.rows, warps, num_sms, SM_WARPS);
-    const size_t shared = can_copy_async<T, W>
-                              ? (size_t)GRAD_STAGES<T, W, K> * 2 * K * rows * warps * 32 * sizeof(Vec<T, W>)
-                              : 0;
-    auto kernel = norm_grad_rows<T, P, W, K>;
+// Row groups (slices) of the gradient's grid at 512 threads per SM.
+int64_t slices_most(int num_sms, const Layout& l) {
+    return (int64_t)num_sms * l.rows * std::max(1, GRAD_THREADS / (l.threads() * l.rows));
+}
+int64_t slices_any(int64_t rows) { return (rows + SLICE_ROWS - 1) / SLICE_ROWS; }
+
+template <typename T, typename P, bool GIVEN>
+cudaError_t norm_grad_launch(const NormGradParams& p, int64_t columns, int num_sms,
+                             cudaStream_t st, int* parts) {
+    constexpr int W = 16 / (int)sizeof(T), K = 16 / W;
+    const Layout l = layout_of(std::min<int64_t>(columns, GRAD_COLUMNS), W, K, 128);
+    const int64_t blocks = blocks_of(p.rows, l.rows, slices_most(num_sms, l) / l.rows, W);
+    const int slices = (int)std::min<int64_t>(p.rows, blocks * l.rows);
+    *parts = l.lanes < 32 ? (int)blocks : slices;
+    const int threads = l.threads() * l.rows;
+    const unsigned tiles = GIVEN ? (unsigned)((columns + GRAD_COLUMNS - 1) / GRAD_COLUMNS) : 1;
+    const size_t shared = (size_t)GRAD_STAGES<T> * 2 * K * threads * 16;
+    auto kernel = norm_grad_rows<T, P, W, K, GIVEN>;
     cudaError_t e = allow_shared(kernel, shared);
     if (e != cudaSuccess) return e;
-    kernel<<<(*slices + rows - 1) / rows, rows * warps * 32, shared, st>>>(p, warps, nvec,
-                                                                          *slices);
+    kernel<<<dim3((unsigned)blocks, tiles), threads, shared, st>>>(p, l, slices);
     return cudaGetLastError();
+}
+
+template <typename F>
+cudaError_t with_types(spmm_type_t type, spmm_type_t param_type, F&& f) {
+    return with_type(type, [&](auto t) {
+        return type == param_type ? f(t, t) : f(t, float{});
+    });
 }
 
 }  // namespace
 
 cudaError_t launch_layer_norm(spmm_type_t type, spmm_type_t param_type, const NormParams& p,
                               int num_sms, cudaStream_t st) {
-    auto typed = [&](auto t, auto pt) {
+    return with_types(type, param_type, [&](auto t, auto pt) {
         using T = decltype(t);
         using P = decltype(pt);
-        constexpr int W = 16 / sizeof(T);
-        const bool wide = p.dim % W == 0 && rows_aligned16(p.x, p.ldx, sizeof(T)) &&
-                          rows_aligned16(p.y, p.ldy, sizeof(T)) &&
-                          (!p.weight || rows_aligned16(p.weight, 0, 1)) &&
-                          (!p.bias || rows_aligned16(p.bias, 0, 1));
-        // A row takes at most 1024 threads.  Few rows leave SMs idle: then the
-        // most threads per row (one access each) give the shortest call; many
-        // rows take four accesses per lane, fewer barriers per byte.
-        if (wide) {
-            const int64_t nvec = p.dim / W;
-            if (nvec <= 1024 && (p.rows <= 2 * num_sms || nvec <= 32))
-                return norm_launch<T, P, W, 1, 0>(p, num_sms, st);
-            if (nvec <= 4096) return norm_launch<T, P, W, 4, 3>(p, num_sms, st);
-        } else {
-            if (p.dim <= 4096) return norm_launch<T, P, 1, 4, 0>(p, num_sms, st);
-            if (p.dim <= 16384) return norm_launch<T, P, 1, 16, 0>(p, num_sms, st);
+        constexpr int W = 16 / (int)sizeof(T);
+        if (alike(p.x, p.ldx, p.y, p.ldy, sizeof(T))) {
+            const bool whole = !off_boundary(p.x, p.ldx, sizeof(T)) && p.dim % W == 0 &&
+                               !(p.weight && reinterpret_cast<uintptr_t>(p.weight) % 16) &&
+                               !(p.bias && reinterpret_cast<uintptr_t>(p.bias) % 16);
+            const int64_t columns = p.dim + W - 1;
+            // Few rows leave SMs idle: then the most threads per row give the shortest
+            // call; many rows take 64 bytes per lane.  Beside binary32 parameters 16-bit
+            // rows are read four elements at a time, so that a warp's parameters, too,
+            // are read from consecutive 16-byte words.
+            const bool few = p.rows <= 2 * num_sms;
+            constexpr int V = sizeof(P) > sizeof(T) ? 4 : W;
+            if (whole) {
+                if (few && p.dim <= 1024 * V)
+                    return norm_launch<T, P, V, 1, true>(p, p.dim, num_sms, st);
+                if (p.dim <= 4096 * W) return norm_launch<T, P, V, 4 * W / V, true>(p, p.dim, num_sms, st);
+            } else {
+                if (few && columns <= 1024 * W)
+                    return norm_launch<T, P, W, 1, false>(p, columns, num_sms, st);
+                // the parameters take 8 bytes of shared memory per column
+                if (columns <= 16384) return norm_launch<T, P, W, 4, false>(p, columns, num_sms, st);
+            }
         }
         const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
-        norm_any<T, P><<<blocks, NORM_THREADS, 0, st>>>(p);
+        norm_any<T, P><<<blocks, ANY_THREADS, 0, st>>>(p);
         return cudaGetLastError();
-    };
-    return with_type(type, [&](auto t) {
-        return type == param_type ? typed(t, t) : typed(t, float{});
     });
 }
 
 size_t norm_grad_scratch(int64_t rows, int64_t dim, int num_sms) {
-    const int64_t slices = std::max(slices_any(rows), slices_rows(rows, 1, num_sms, SM_WARPS_MOST));
-    return (size_t)slices * 2 * (size_t)dim * sizeof(float);
+    // a row group per warp at most; and the rows' means
+    const int64_t slices = std::max(
+        slices_any(rows), std::min<int64_t>(rows, (int64_t)num_sms * (GRAD_THREADS / 32)));
+    return ((size_t)slices * 2 * (size_t)dim + (size_t)rows * 2) * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,
-                                   const NormGradParams& p, int num_sms, cudaStream_t st) {
-    auto typed = [&](auto t, auto pt) {
+                                   const NormGradParams& given, int num_sms, cudaStream_t st) {
+    return with_types(type, param_type, [&](auto t, auto pt) {
         using T = decltype(t);
         using P = decltype(pt);
-        constexpr int W = 16 / sizeof(T);
-        constexpr int K = 16 / W;                     // 16 elements of the row per lane
+        constexpr int W = 16 / (int)sizeof(T);
+        NormGradParams p = given;
         const bool sums = p.dweight || p.dbias;
+        p.means = p.part;
+        p.part = sums ? p.means + 2 * p.rows : nullptr;
         int slices = 0;
         cudaError_t e = cudaSuccess;
         if (p.rows > 0) {
-            const bool wide = p.dim % W == 0 && rows_aligned16(p.x, p.ldx, sizeof(T)) &&
-                              rows_aligned16(p.dy, p.ld_dy, sizeof(T)) &&
-                              rows_aligned16(p.dx, p.ld_dx, sizeof(T)) &&
-                              (!p.weight || rows_aligned16(p.weight, 0, 1));
-            if (wide && p.dim <= NORM_GRAD_THREADS * 16) {
-                e = norm_grad_launch<T, P, W, K>(p, num_sms, st, &slices);
-            } else if (p.dim <= NORM_GRAD_THREADS * 4) {
-                e = norm_grad_launch<T, P, 1, 4>(p, num_sms, st, &slices);
-            } else if (p.dim <= NORM_GRAD_THREADS * 8) {
-                e = norm_grad_launch<T, P, 1, 8>(p, num_sms, st, &slices);
-            } else if (p.dim <= NORM_GRAD_THREADS * 16) {
-                e = norm_grad_launch<T, P, 1, 16>(p, num_sms, st, &slices);
+            const int64_t columns = p.dim + (off_boundary(p.x, p.ldx, sizeof(T)) ? W - 1 : 0);
+            const bool same = alike(p.x, p.ldx, p.dy, p.ld_dy, sizeof(T)) &&
+                              alike(p.x, p.ldx, p.dx, p.ld_dx, sizeof(T));
+            if (same && columns <= GRAD_COLUMNS) {
+                e = norm_grad_launch<T, P, false>(p, columns, num_sms, st, &slices);
             } else {
-                // the sums first: dx may be dy
-                slices = (int)slices_any(p.rows);
-                if (sums) {
-                    const dim3 grid((unsigned)((p.dim + 31) / 32), (unsigned)slices);
-                    norm_dw_any<T><<<grid, 256, 0, st>>>(p);
-                }
                 const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
-                norm_dx_any<T, P><<<blocks, NORM_THREADS, 0, st>>>(p);
+                grad_means<T, P><<<blocks, ANY_THREADS, 0, st>>>(p);
                 e = cudaGetLastError();
+                if (e != cudaSuccess) return e;
+                if (same) {
+                    e = norm_grad_launch<T, P, true>(p, columns, num_sms, st, &slices);
+                } else {
+                    slices = (int)slices_any(p.rows);
+                    const dim3 grid((unsigned)((p.dim + ANY_THREADS - 1) / ANY_THREADS),
+                                    (unsigned)slices);
+                    norm_grad_any<T, P><<<grid, ANY_THREADS, 0, st>>>(p);
+                    e = cudaGetLastError();
+                }
             }
         }
         if (e != cudaSuccess || !sums) return e;
         return launch_chained(norm_dw_join<P>, dim3((unsigned)((p.dim + 31) / 32), 2),
                               dim3(32 * JOIN_WARPS), 0, st, p.rows > 0, p, slices);
-    };
-    return with_type(type, [&](auto t) {
-        return type == param_type ? typed(t, t) : typed(t, float{});
     });
 }
 

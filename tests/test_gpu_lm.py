@@ -40,6 +40,13 @@ def _make(rng, shape, t, scale=1.0, shift=0.0, pad=0, offset=0):
     return out, view.double().numpy()
 
 
+def _like(x, offset):
+    """An uninitialised matrix that lies in its buffer as `x`, made with `offset`, does."""
+    rows, ld = x.shape[0], x.stride(0)
+    buf = torch.empty(offset + rows * ld, dtype=x.dtype, device="cuda")
+    return buf[offset:].view(rows, ld)[:, :x.shape[1]]
+
+
 def _vec(rng, n, t, scale=1.0, shift=0.0):
     v, h = _make(rng, (1, n), t, scale, shift)
     return v[0].contiguous(), h[0]
@@ -225,8 +232,10 @@ def test_layer_norm(cs, handle, t, pt, rows, dim, pad, offset):
         _near(_np(g), want, bound, what)
     plain = cs.layer_norm(handle, x, eps=1e-3)
     _near(_np(plain[0]), *ref.layer_norm(h_x, 1.0, 0.0, float(np.float32(1e-3)), t)[0], "no weight")
+    apart = cs.layer_norm(handle, x, w, b, eps=1e-3, out=_like(x, offset))[0]
     y = cs.layer_norm(handle, x, w, b, eps=1e-3, out=x)[0]
-    assert y.data_ptr() == x.data_ptr() and torch.equal(y, got[0]), "in place"
+    assert y.data_ptr() == x.data_ptr() and torch.equal(y, apart), "in place"
+    _near(_np(y), *ref.layer_norm(h_x, h_w, h_b, float(np.float32(1e-3)), t)[0], "in place")
 
 
 @pytest.mark.parametrize("dim", [64, 1001, 4096, 20000])
@@ -274,9 +283,12 @@ def test_layer_norm_grad(cs, handle, t, pt, rows, dim, pad, offset):
     plain = cs.layer_norm_grad(handle, dy, x, mean, rstd, bias=False)
     assert plain[1] is None and plain[2] is None
     _near(_np(plain[0]), *ref.layer_norm_grad(h_dy, h_x, h_mean, h_rstd, 1.0, t, pt)[0], "dx")
+    apart = cs.layer_norm_grad(handle, dy, x, mean, rstd, w, out=_like(dy, 0))
     again = cs.layer_norm_grad(handle, dy, x, mean, rstd, w, out=dy)
-    for a, b in zip(again, got):
+    for a, b in zip(again, apart):
         assert torch.equal(a, b), "in place, and the same bits again"
+    for g, (v, bound), what in zip(again, want, ("dx", "dweight", "dbias")):
+        _near(_np(g), v, bound, what)
 
 
 def test_layer_norm_gradient_against_differences(cs, handle):
