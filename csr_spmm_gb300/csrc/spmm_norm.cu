@@ -68,16 +68,20 @@ template <typename P, int W>
 __device__ __forceinline__ Vec<P, W> load_params(const void* p, int c, int dim, float none) {
     if (!p) {
         Vec<P, W> r;
-        const float f[2] = {none, none};
+        if constexpr (W == 1) {
+            r.w = from_f32<P>(none);
+        } else {
+            const float f[2] = {none, none};
 #pragma unroll
-        for (int i = 0; i < Vec<P, W>::WORDS; ++i) {
-            if constexpr (sizeof(P) == 4) r.w[i] = __float_as_uint(none);
-            else r.w[i] = pack_word(f, P{});
+            for (int i = 0; i < Vec<P, W>::WORDS; ++i) {
+                if constexpr (sizeof(P) == 4) r.w[i] = __float_as_uint(none);
+                else r.w[i] = pack_word(f, P{});
+            }
         }
         return r;
     }
     const P* from = static_cast<const P*>(p);
-    if (c >= 0 && c + W <= dim && reinterpret_cast<uintptr_t>(from + c) % 16 == 0)
+    if (W > 1 && c >= 0 && c + W <= dim && reinterpret_cast<uintptr_t>(from + c) % 16 == 0)
         return load_vec<Cache::KEEP, P, W>(from + c);
     return load_some<P, W>(from, c, dim);
 }
@@ -105,6 +109,8 @@ struct Rows {
     __device__ Rows(const void* p, int64_t ld, int64_t rows, int64_t dim)
         : base(static_cast<const T*>(p)), ld(ld), end(base + (rows - 1) * ld + dim), dim((int)dim) {}
     __device__ const T* row(int64_t r) const { return base + r * ld; }
+    // whether an access to row r may reach over the matrix's ends
+    __device__ bool at_ends(int64_t r, int64_t rows) const { return r < W || r >= rows - W; }
     __device__ bool inside(const T* row, int c) const {
         return (c >= 0 && c + W <= dim) || (row + c >= base && row + c + W <= end);
     }
@@ -113,12 +119,29 @@ struct Rows {
     }
     __device__ void copy(Vec<T, W>* to, const T* row, int c) const {
         if (inside(row, c)) copy_async<T, W>(to, row + c);
-    }
-    // what copy() sent, or could not send
-    __device__ Vec<T, W> take(const Vec<T, W>* from, const T* row, int c) const {
-        return inside(row, c) ? *from : load_some<T, W>(row, c, dim);
+        else *to = load_some<T, W>(row, c, dim);
     }
 };
+// The bits of an access's elements that belong to the row.
+template <typename T, int W>
+__device__ __forceinline__ Vec<T, W> mask_of(int c, int dim) {
+    Vec<T, W> r;
+#pragma unroll
+    for (int i = 0; i < Vec<T, W>::WORDS; ++i) r.w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        if (c + i >= 0 && c + i < dim) {
+            if constexpr (sizeof(T) == 4) r.w[i] = 0xffffffffu;
+            else r.w[i / 2] |= 0xffffu << ((i & 1) * 16);
+        }
+    return r;
+}
+template <typename T, int W>
+__device__ __forceinline__ Vec<T, W> masked(Vec<T, W> v, const Vec<T, W>& mask, uint32_t all) {
+#pragma unroll
+    for (int i = 0; i < Vec<T, W>::WORDS; ++i) v.w[i] &= mask.w[i] & all;
+    return v;
+}
 template <typename T, int W>
 __device__ __forceinline__ void store_some(T* row, int c, int dim, const float (&f)[W]) {
     if (c >= 0 && c + W <= dim) {
@@ -196,13 +219,18 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
         Vec<T, W> held[K];
         int own = 0;                             // elements of the row in this lane
         auto in = [&](int k) { return FIT == Fit::ALL || (live && c0 + k * step < dim); };
+        if (EDGES && x.at_ends(r, p.rows)) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = c0 + k * step;
-            if (!in(k)) continue;
-            held[k] = EDGES ? x.load(row, c) : load_vec<Cache::STREAM, T, W>(row + c);
-            own += EDGES ? min(c + W, dim) - max(c, 0) : W;
+            for (int k = 0; k < K; ++k)
+                if (in(k)) held[k] = x.load(row, c0 + k * step);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (in(k)) held[k] = load_vec<Cache::STREAM, T, W>(row + c0 + k * step);
         }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (in(k)) own += EDGES ? min(c0 + k * step + W, dim) - max(c0 + k * step, 0) : W;
         uint64_t sums = pair(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -351,6 +379,10 @@ constexpr int GRAD_COLUMNS = GRAD_THREADS * 16;
 template <typename T>
 constexpr int GRAD_STAGES = sizeof(T) == 4 ? 3 : 4;
 
+// Elements outside the row (EDGES: any row whose threads' accesses are not all whole and in
+// it) are masked, not branched around: a branch per access kept the others waiting
+// (32,768 x 4096 bf16: 219 us with them, 142 without).
+//
 // dx, and this group's share of dweight and dbias, in one pass over dy and x: a row's
 // threads walk the rows with a fixed stride, the rows ahead on their way to shared
 // memory (each lane's accesses in slots of its own), and keep their columns' sums of
@@ -358,10 +390,11 @@ constexpr int GRAD_STAGES = sizeof(T) == 4 ? 3 : 4;
 // columns, in tiles of as many (blockIdx.y); the row's two means come from
 // grad_means and nothing is exchanged.  The bound is HBM (read dy and x, write dx).
 // part: [slices, or blocks of narrow rows][2][dim].
-template <typename T, typename P, int W, int K, bool GIVEN>
+template <typename T, typename P, int W, int K, Fit FIT, bool GIVEN>
 __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p, Layout l,
                                                                int slices) {
     constexpr int STAGES = GRAD_STAGES<T>;
+    constexpr bool EDGES = FIT == Fit::EDGES;
     __shared__ float2 slots[2][32];
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     Vec<T, W>* ring = reinterpret_cast<Vec<T, W>*>(ring_bytes) + threadIdx.x;
@@ -373,17 +406,37 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
     const int slice = blockIdx.x * l.rows + in_block;
     int64_t r = slice, first = r - lane / l.lanes;
     // the tile's accesses follow the ones of the tiles before, so none is in two tiles
-    const int c0 = tid * W - lead_of<T, W>(x.row(r)) + (GIVEN ? (int)blockIdx.y * GRAD_COLUMNS : 0);
+    const int c0 = tid * W - (EDGES ? lead_of<T, W>(x.row(r)) : 0) + (GIVEN ? (int)blockIdx.y * GRAD_COLUMNS : 0);
     const int step = threads * W;
+    auto in = [&](int k) { return FIT == Fit::ALL || c0 + k * step < dim; };
     auto fetch = [&](int64_t row, int stage) {
+        if (row < p.rows) {
+            const T* xr = x.row(row);
+            const T* dyr = dy.row(row);
+            Vec<T, W>* to = ring + stage * 2 * K * blockDim.x;
+            if (EDGES && x.at_ends(row, p.rows)) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (row < p.rows && c0 + k * step < dim) {
-                x.copy(ring + (stage * 2 * K + k) * blockDim.x, x.row(row), c0 + k * step);
-                dy.copy(ring + (stage * 2 * K + K + k) * blockDim.x, dy.row(row), c0 + k * step);
+                for (int k = 0; k < K; ++k) {
+                    if (!in(k)) continue;
+                    x.copy(to + k * blockDim.x, xr, c0 + k * step);
+                    dy.copy(to + (K + k) * blockDim.x, dyr, c0 + k * step);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (!in(k)) continue;
+                    copy_async<T, W>(to + k * blockDim.x, xr + c0 + k * step);
+                    copy_async<T, W>(to + (K + k) * blockDim.x, dyr + c0 + k * step);
+                }
             }
+        }
         copies_issued();
     };
+    // the masks follow the ring
+    Vec<T, W>* mask = ring + STAGES * 2 * K * blockDim.x;
+    if (EDGES)
+#pragma unroll
+        for (int k = 0; k < K; ++k) mask[k * blockDim.x] = mask_of<T, W>(c0 + k * step, dim);
     // slices beyond the grid's last row group have no rows (slice >= slices)
     const int64_t rows = slice - lane / l.lanes < slices ? p.rows : 0;
     if (rows > 0)
@@ -394,7 +447,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
     for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) dw[k][i] = db[k][i] = pair(0.0f, 0.0f);
-        if (c0 + k * step < dim) w[k] = load_params<P, W>(p.weight, c0 + k * step, dim, 1.0f);
+        w[k] = load_params<P, W>(p.weight, c0 + k * step, dim, 1.0f);
     }
     const float per_dim = 1.0f / (float)dim;
     int turn = 0, stage = 0;
@@ -409,7 +462,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
     };
     statistics(r);
     for (; first < rows; first += slices, r += slices) {
-        const bool live = r < rows && slice < slices;
+        const bool live = FIT == Fit::ALL || (r < rows && slice < slices);
         const float mean = next_mean, rstd = next_rstd;
         const float2 ab = next_ab;
         statistics(r + slices);
@@ -419,13 +472,16 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
         const uint64_t m2 = pair(-mean, -mean), r2 = pair(rstd, rstd);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = c0 + k * step;
-            if (!live || c >= dim) continue;
             float xf[W], gf[W], wf[W];
-            unpack(x.take(ring + (stage * 2 * K + k) * blockDim.x, x.row(r), c), xf);
-            unpack(dy.take(ring + (stage * 2 * K + K + k) * blockDim.x, dy.row(r), c), gf);
-            clear_outside(c, dim, gf);
-            clear_outside(c, dim, xf);
+            const Vec<T, W>* from = ring + (stage * 2 * K + k) * blockDim.x;
+            if constexpr (EDGES) {
+                const uint32_t all = live ? ~0u : 0u;
+                unpack(masked(*from, mask[k * blockDim.x], all), xf);
+                unpack(masked(from[K * blockDim.x], mask[k * blockDim.x], all), gf);
+            } else {
+                unpack(*from, xf);
+                unpack(from[K * blockDim.x], gf);
+            }
             unpack(w[k], wf);
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
@@ -474,18 +530,33 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = c0 + k * step;
-            if (c >= dim) continue;
+            if (!in(k)) continue;
             float f[W];
 #pragma unroll
             for (int i = 0; i < W / 2; ++i)
                 halves(mul2(r2, fma2(nb, xh[k][i], add2(g[k][i], na))), f[2 * i], f[2 * i + 1]);
-            store_some<T, W>(dx, c, dim, f);
+            if (EDGES) store_some<T, W>(dx, c, dim, f);
+            else store_vec<Cache::STREAM, T, W>(dx + c, f);
         }
     }
     allow_successor();
     if (!p.part) return;
-    // one part per row group; narrow rows, many to a block, are first added up there
+    // one part per row group; narrow rows, many to a block, are first added up there: over
+    // the warp's lanes where they have the same columns, then one after the other in
+    // shared memory
     const bool narrow = l.lanes < 32;
+    bool mine = slice < slices;
+    if (narrow && __all_sync(ALL, c0 == (lane & (l.lanes - 1)) * W)) {
+        for (int o = l.lanes; o < 32; o <<= 1)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) {
+                    dw[k][i] = add2(dw[k][i], __shfl_xor_sync(ALL, dw[k][i], o));
+                    db[k][i] = add2(db[k][i], __shfl_xor_sync(ALL, db[k][i], o));
+                }
+        mine = lane < l.lanes;
+    }
     float* part = p.part + (int64_t)(narrow ? blockIdx.x : slice) * 2 * p.dim;
     if (narrow) {
         copies_wait<0>();
@@ -493,23 +564,38 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
         part = reinterpret_cast<float*>(ring_bytes);
         for (int i = threadIdx.x; i < 2 * dim; i += blockDim.x) part[i] = 0.0f;
     }
-    for (int turn_of = 0; turn_of < (narrow ? l.rows : 1); ++turn_of) {
-        if (narrow) __syncthreads();
-        if (slice >= slices || (narrow && turn_of != in_block)) continue;
+    for (int group = 0; group < (narrow ? l.rows : 1); ++group) {
+        if (narrow) {
+            if (!__syncthreads_or(group == in_block && mine)) continue;
+            if (group != in_block) continue;
+        }
+        if (!mine) continue;
+        float sums[2][K][W];
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
-                const int c = c0 + k * step + 2 * i;
-                float wf[2], bf[2];
-                halves(dw[k][i], wf[0], wf[1]);
-                halves(db[k][i], bf[0], bf[1]);
+                halves(dw[k][i], sums[0][k][2 * i], sums[0][k][2 * i + 1]);
+                halves(db[k][i], sums[1][k][2 * i], sums[1][k][2 * i + 1]);
+            }
+        if (narrow)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (c + e < 0 || c + e >= dim) continue;
-                    part[c + e] = narrow ? part[c + e] + wf[e] : wf[e];
-                    part[dim + c + e] = narrow ? part[dim + c + e] + bf[e] : bf[e];
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const int c = c0 + k * step + i;
+                    if (c < 0 || c >= dim) continue;
+                    sums[0][k][i] += part[c];
+                    sums[1][k][i] += part[dim + c];
                 }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const int c = c0 + k * step + i;
+                if (c < 0 || c >= dim) continue;
+                part[c] = sums[0][k][i];
+                part[dim + c] = sums[1][k][i];
             }
     }
     if (narrow) {
@@ -519,23 +605,45 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
     }
 }
 
-// The two means of each row, element by element: a block per row.
-template <typename T, typename P>
+// The two means of each row: a block per row.  W == 1 where x and dy lie differently
+// against 16-byte boundaries.
+template <typename T, typename P, int W>
 __global__ __launch_bounds__(ANY_THREADS) void grad_means(NormGradParams p) {
     __shared__ float s[ANY_THREADS / 32];
+    const Rows<T, W> x(p.x, p.ldx, p.rows, p.dim), dy(p.dy, p.ld_dy, p.rows, p.dim);
+    const int dim = (int)p.dim;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const T* x = static_cast<const T*>(p.x) + r * p.ldx;
-        const T* dy = static_cast<const T*>(p.dy) + r * p.ld_dy;
+        const T* xr = x.row(r);
+        const T* dyr = dy.row(r);
+        const int lead = W > 1 ? lead_of<T, W>(xr) : 0;
         const float mean = p.mean[r], rstd = p.rstd[r];
         float a = 0.0f, b = 0.0f;
-#pragma unroll 4
-        for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) {
-            const float g = to_f32(dy[c]) * param<P>(p.weight, c, 1.0f);
-            a += g;
-            b += g * ((to_f32(x[c]) - mean) * rstd);
+        for (int c = threadIdx.x * W - lead; c < dim; c += 2 * ANY_THREADS * W) {
+            Vec<T, W> xv[2], dyv[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int at = c + u * ANY_THREADS * W;
+                const bool whole = at >= 0 && at + W <= dim;
+                xv[u] = whole ? load_vec<Cache::KEEP, T, W>(xr + at) : load_some<T, W>(xr, at, dim);
+                dyv[u] = whole ? load_vec<Cache::KEEP, T, W>(dyr + at)
+                               : load_some<T, W>(dyr, at, dim);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float xf[W], gf[W], wf[W];
+                unpack(xv[u], xf);
+                unpack(dyv[u], gf);
+                unpack(load_params<P, W>(p.weight, c + u * ANY_THREADS * W, dim, 1.0f), wf);
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const float g = gf[i] * wf[i];   // 0 outside the row
+                    a += g;
+                    b = fmaf(g, (xf[i] - mean) * rstd, b);
+                }
+            }
         }
-        a = block_sum(a, s) / (float)p.dim;
-        b = block_sum(b, s) / (float)p.dim;
+        a = block_sum(a, s) / (float)dim;
+        b = block_sum(b, s) / (float)dim;
         if (threadIdx.x == 0) reinterpret_cast<float2*>(p.means)[r] = make_float2(a, b);
     }
 }
@@ -670,8 +778,12 @@ cudaError_t norm_grad_launch(const NormGradParams& p, int64_t columns, int num_s
     *parts = l.lanes < 32 ? (int)blocks : slices;
     const int threads = l.threads() * l.rows;
     const unsigned tiles = GIVEN ? (unsigned)((columns + GRAD_COLUMNS - 1) / GRAD_COLUMNS) : 1;
-    const size_t shared = (size_t)GRAD_STAGES<T> * 2 * K * threads * 16;
-    auto kernel = norm_grad_rows<T, P, W, K, GIVEN>;
+    // the ring, and masks for rows with edges
+    const size_t shared = ((size_t)GRAD_STAGES<T> * 2 + 1) * K * threads * 16;
+    const bool all = columns == p.dim && l.lanes == 32 &&
+                     p.dim == (int64_t)tiles * l.threads() * W * K;
+    auto kernel = all ? norm_grad_rows<T, P, W, K, Fit::ALL, GIVEN>
+                      : norm_grad_rows<T, P, W, K, Fit::EDGES, GIVEN>;
     cudaError_t e = allow_shared(kernel, shared);
     if (e != cudaSuccess) return e;
     kernel<<<dim3((unsigned)blocks, tiles), threads, shared, st>>>(p, l, slices);
@@ -748,7 +860,10 @@ cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,
                 e = norm_grad_launch<T, P, false>(p, columns, num_sms, st, &slices);
             } else {
                 const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
-                grad_means<T, P><<<blocks, ANY_THREADS, 0, st>>>(p);
+                if (alike(p.x, p.ldx, p.dy, p.ld_dy, sizeof(T)))
+                    grad_means<T, P, W><<<blocks, ANY_THREADS, 0, st>>>(p);
+                else
+                    grad_means<T, P, 1><<<blocks, ANY_THREADS, 0, st>>>(p);
                 e = cudaGetLastError();
                 if (e != cudaSuccess) return e;
                 if (same) {
