@@ -20,33 +20,36 @@ constexpr int EMBED_THREADS = 256;
 constexpr int EMBED_BATCH = 4;       // accesses in flight per thread
 
 // A block takes `block_rows` rows; its threads walk the rows' accesses in
-// order (nv accesses of W elements per row, then the next row), so narrow
+// order (nv accesses of 16 bytes per row, then the next row), so narrow
 // rows share a warp and the stores of neighbouring threads are contiguous.
-// The bound is HBM: one table row read and one written per token.
-template <typename T, int W>
+// EDGES: any width and alignment: accesses are those of out's aligned words, and
+// the table is read from wherever their elements lie.  The bound is HBM: one table
+// row read and one written per token.
+template <typename T, bool EDGES>
 __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int nv,
                                                             int block_rows) {
+    constexpr int W = 16 / (int)sizeof(T);
     const T* table = static_cast<const T*>(p.table);
-    T* out = static_cast<T*>(p.out);
     const int64_t row0 = (int64_t)blockIdx.x * block_rows;
+    const int* ids = p.ids + row0;
+    T* out = static_cast<T*>(p.out) + row0 * p.ld_out;
     const int rows = (int)min((int64_t)block_rows, p.tokens - row0);
+    const int dim = (int)p.dim;
+    const int64_t elements = (p.vocab - 1) * p.ld_table + p.dim;
     const int step_r = EMBED_THREADS / nv, step_c = EMBED_THREADS % nv;
     int r = threadIdx.x / nv, c = threadIdx.x % nv;
     while (r < rows) {
+        // ids, then rows, each for the whole batch and none behind a branch (past the
+        // block's rows and for padding some row is read in vain), so that all are
+        // on their way together
+        int id[EMBED_BATCH], row[EMBED_BATCH], col[EMBED_BATCH];
         Vec<T, W> v[EMBED_BATCH];
-        int64_t to[EMBED_BATCH];
-        bool valid[EMBED_BATCH];
+        Unaligned<T> far[EDGES ? EMBED_BATCH : 1];
 #pragma unroll
         for (int u = 0; u < EMBED_BATCH; ++u) {
-            to[u] = -1;
-            if (r < rows) {
-                const int64_t row = row0 + r;
-                const int id = p.ids[row];
-                to[u] = row * p.ld_out + (int64_t)c * W;
-                valid[u] = id >= 0 && id < p.vocab;
-                if (valid[u])
-                    v[u] = load_vec<Cache::KEEP, T, W>(table + id * p.ld_table + (int64_t)c * W);
-            }
+            row[u] = r;
+            col[u] = c * W;
+            id[u] = ids[min(r, rows - 1)];
             r += step_r;
             c += step_c;
             if (c >= nv) {
@@ -54,27 +57,67 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int n
                 ++r;
             }
         }
+        if (p.vocab > 0) {
+            if constexpr (EDGES) {
+                bool clear = true;
+                int64_t at[EMBED_BATCH];
+#pragma unroll
+                for (int u = 0; u < EMBED_BATCH; ++u) {
+                    const bool valid = id[u] >= 0 && id[u] < p.vocab;
+                    col[u] -= lead_of(out + min(row[u], rows - 1) * p.ld_out, 16);
+                    at[u] = (valid ? id[u] : p.vocab / 2) * p.ld_table + min(col[u], dim - 1);
+                    clear &= clear_of_ends<W>(at[u], elements);
+                }
+                if (clear) {
+#pragma unroll
+                    for (int u = 0; u < EMBED_BATCH; ++u) far[u].load(table + at[u]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < EMBED_BATCH; ++u) {
+                        const bool valid = id[u] >= 0 && id[u] < p.vocab;
+                        far[u].a = load_some<T, W>(table + (valid ? id[u] : 0) * p.ld_table,
+                                                   col[u], dim);
+                        far[u].b = far[u].a;
+                        far[u].shift = 0;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < EMBED_BATCH; ++u) {
+                    const bool valid = id[u] >= 0 && id[u] < p.vocab;
+                    v[u] = load_vec<Cache::KEEP, T, W>(table + (valid ? id[u] : 0) * p.ld_table +
+                                                       col[u]);
+                }
+            }
+        }
 #pragma unroll
         for (int u = 0; u < EMBED_BATCH; ++u) {
-            if (to[u] < 0) continue;
+            if (row[u] >= rows) continue;
+            const bool valid = id[u] >= 0 && id[u] < p.vocab;
             float f[W];
-            unpack(v[u], f);
+            unpack(EDGES ? far[EDGES ? u : 0].get() : v[u], f);
 #pragma unroll
-            for (int i = 0; i < W; ++i) f[i] = valid[u] ? p.scale * f[i] : 0.0f;
-            store_vec<Cache::STREAM, T, W>(out + to[u], f);
+            for (int i = 0; i < W; ++i) f[i] = valid ? p.scale * f[i] : 0.0f;
+            if (EDGES) store_some<T, W>(out + row[u] * p.ld_out, col[u], dim, f);
+            else store_vec<Cache::STREAM, T, W>(out + row[u] * p.ld_out + col[u], f);
         }
     }
 }
 
-template <typename T, int W>
+template <typename T>
 cudaError_t launch_embed(const EmbedParams& p, int num_sms, cudaStream_t st) {
-    const int nv = (int)(p.dim / W);
+    constexpr int W = 16 / (int)sizeof(T);
+    const bool whole = p.dim % W == 0 && rows_aligned16(p.out, p.ld_out, sizeof(T)) &&
+                       (p.vocab == 0 || rows_aligned16(p.table, p.ld_table, sizeof(T)));
+    // a row between boundaries covers up to W - 1 elements more
+    const int nv = (int)((p.dim + (whole ? 0 : 2 * (W - 1))) / W);
     // about 8 accesses per thread and block; fewer rows per block while that
     // would leave SMs without a block
     int64_t rows = std::max<int64_t>(1, EMBED_THREADS * 8 / nv);
     rows = std::max<int64_t>(1, std::min<int64_t>(rows, p.tokens / (4 * num_sms)));
-    const int64_t blocks = (p.tokens + rows - 1) / rows;
-    embed_rows<T, W><<<(unsigned)blocks, EMBED_THREADS, 0, st>>>(p, nv, (int)rows);
+    const unsigned blocks = (unsigned)((p.tokens + rows - 1) / rows);
+    if (whole) embed_rows<T, false><<<blocks, EMBED_THREADS, 0, st>>>(p, nv, (int)rows);
+    else embed_rows<T, true><<<blocks, EMBED_THREADS, 0, st>>>(p, nv, (int)rows);
     return cudaGetLastError();
 }
 
@@ -82,7 +125,7 @@ cudaError_t launch_embed(const EmbedParams& p, int num_sms, cudaStream_t st) {
 
 constexpr int SORT_TILE = 512;       // keys sorted by one block, one per thread
 constexpr int MERGE_WAYS = 16;       // sorted runs merged per round
-constexpr unsigned NO_ID = 0xffffffffu;
+constexpr unsigned NO_ID = 0xfffffffeu;  // of padding; one more is still a number
 
 // Sorts each tile of SORT_TILE tokens with a bitonic network, one 64-bit key per
 // thread: exchanges within a warp are shuffles (35 of the 45 steps), the others
@@ -139,40 +182,45 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
     return lo;
 }
 
-// Merges groups of MERGE_WAYS sorted runs of `run` keys (a power of two): keys
-// are unique, so each key's place is the count of smaller keys over the group's
-// runs.  The searches of all runs take their steps together, MERGE_WAYS loads
-// at a time: a step costs one latency, not one for each run (65,536 keys:
-// 35 us per round with one search after the other).
-__global__ __launch_bounds__(256) void merge_runs(const uint64_t* in, uint64_t* out, int tokens,
-                                                  int64_t run) {
+// Merges groups of MERGE_WAYS sorted runs of `run` keys (a power of two): each key's
+// place is the count of smaller keys over the group's runs.  An earlier run holds
+// earlier tokens, so of equal ids those of earlier runs count, and the ids alone
+// decide.  The searches of all runs take their steps together, MERGE_WAYS loads
+// at a time and none behind a branch: a step costs one latency, not one for each run.
+__global__ __launch_bounds__(256) void merge_runs(const uint64_t* __restrict__ in,
+                                                  uint64_t* __restrict__ out, int tokens, int run) {
     allow_successor();
     wait_for_predecessor();
-    const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int g = blockIdx.x * 256 + threadIdx.x;
     if (g >= tokens) return;
     const uint64_t key = in[g];
-    const int64_t first = g / (run * MERGE_WAYS) * (run * MERGE_WAYS);
-    int64_t below[MERGE_WAYS];       // per run: start + keys known to be smaller
+    const unsigned id = (unsigned)(key >> 32);
+    const unsigned* ids = reinterpret_cast<const unsigned*>(in) + 1;     // of key i at 2 i
+    const int last = tokens - 1;
+    // tokens <= 2^30: every start that matters fits 31 bits
+    const int64_t first = g / ((int64_t)run * MERGE_WAYS) * run * MERGE_WAYS;
+    const int own = (int)((g - first) / run);
+    int start[MERGE_WAYS], below[MERGE_WAYS];
 #pragma unroll
-    for (int q = 0; q < MERGE_WAYS; ++q) below[q] = first + q * run;
-    for (int64_t half = run >> 1; half > 0; half >>= 1) {
-        uint64_t got[MERGE_WAYS];
+    for (int q = 0; q < MERGE_WAYS; ++q)
+        start[q] = below[q] = (int)min(first + (int64_t)q * run, (int64_t)tokens);
+    for (int half = run >> 1; half > 0; half >>= 1) {
+        unsigned got[MERGE_WAYS];
 #pragma unroll
-        for (int q = 0; q < MERGE_WAYS; ++q) {
-            const int64_t at = below[q] + half - 1;
-            got[q] = at < tokens ? in[at] : ~0ull;
-        }
+        for (int q = 0; q < MERGE_WAYS; ++q) got[q] = __ldg(ids + 2 * (int64_t)min(below[q] + half - 1, last));
 #pragma unroll
         for (int q = 0; q < MERGE_WAYS; ++q)
-            if (got[q] < key) below[q] += half;
+            if (below[q] + half - 1 <= last && got[q] < id + (q < own)) below[q] += half;
     }
     // one candidate is left in each run
-    int64_t place = first;
+    unsigned got[MERGE_WAYS];
+    int place = (int)first;
 #pragma unroll
-    for (int q = 0; q < MERGE_WAYS; ++q) {
-        const int64_t at = below[q];
-        place += at - (first + q * run) + (at < tokens && in[at] < key);
-    }
+    for (int q = 0; q < MERGE_WAYS; ++q) got[q] = __ldg(ids + 2 * (int64_t)min(below[q], last));
+#pragma unroll
+    for (int q = 0; q < MERGE_WAYS; ++q)
+        place += q == own ? g - start[q]
+                          : below[q] - start[q] + (below[q] <= last && got[q] < id + (q < own));
     out[place] = key;
 }
 
@@ -197,7 +245,8 @@ inline int piece_of(int64_t tokens, int64_t dim) {
     while (piece < PIECE_MAX && tokens * panels_of(dim) / piece > SUM_WARPS) piece *= 2;
     return piece;
 }
-inline int64_t padded(int64_t dim) { return (dim + 7) / 8 * 8; }   // partial rows: 32 bytes
+// A partial row: whole accesses of 32 bytes, one more for rows between boundaries.
+inline int64_t padded(int64_t dim) { return (dim + 7) / 8 * 8 + 8; }
 
 struct GradWork {
     const uint64_t* keys;            // sorted
@@ -226,49 +275,73 @@ __device__ __forceinline__ int warp_count_below(const uint64_t* a, int n, uint64
 }
 
 // W elements per access, V accesses per lane and row segment: W * V * 32 == PANEL.
-template <typename T, typename G, int W, int V, int BATCH>
+// EDGES: any width and alignment: accesses are those of the table row's aligned words
+// (its first begins `lead` columns before it), and dout is read from wherever their
+// elements lie.
+template <typename T, typename G, int W, int V, int BATCH, bool EDGES>
 struct GradSum {
     static_assert(W * V * 32 == PANEL);
     const EmbedGradParams& p;
     const GradWork& k;
     int lane;
-    int64_t col;                     // the panel's first column
+    int col;                         // the panel's first column
+    int dim;
+    int lead;                        // of the row being summed
     float acc[V][W];
 
-    __device__ bool inside(int v) const { return col + (v * 32 + lane) * W < p.dim; }
-    __device__ void clear() {
+    __device__ G* row_of(unsigned id) const {
+        return static_cast<G*>(p.dtable) + (int64_t)id * p.ld_dtable;
+    }
+    __device__ int lead_for(unsigned id) const { return EDGES ? lead_of(row_of(id), 16) : 0; }
+    __device__ int column(int v, int lead) const { return col + (v * 32 + lane) * W - lead; }
+    __device__ void begin(unsigned id) {
+        lead = lead_for(id);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[v][i] = 0.0f;
     }
     // dtable[row] = beta * dtable[row] + scale * acc
-    __device__ void finish(unsigned row) {
-        G* to = static_cast<G*>(p.dtable) + (int64_t)row * p.ld_dtable + col + lane * W;
+    __device__ void finish(unsigned id) {
+        G* to = row_of(id);
+        Vec<G, W> old[V];
+        if (p.beta != 0.0f)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                // past the row column 0 is read in vain: an access behind a branch would
+                // keep the others waiting
+                const int c = column(v, lead);
+                if constexpr (EDGES)
+                    old[v] = c >= 0 && c + W <= dim ? load_vec<Cache::STREAM, G, W>(to + c)
+                                                    : load_some<G, W>(to, c, dim);
+                else
+                    old[v] = load_vec<Cache::STREAM, G, W>(to + (c < dim ? c : 0));
+            }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (!inside(v)) continue;
             float f[W];
 #pragma unroll
             for (int i = 0; i < W; ++i) f[i] = p.scale * acc[v][i];
             if (p.beta != 0.0f) {
-                float old[W];
-                unpack(load_vec<Cache::STREAM, G, W>(to + v * 32 * W), old);
+                float o[W];
+                unpack(old[v], o);
 #pragma unroll
-                for (int i = 0; i < W; ++i) f[i] += p.beta * old[i];
+                for (int i = 0; i < W; ++i) f[i] += p.beta * o[i];
             }
-            store_vec<Cache::STREAM, G, W>(to + v * 32 * W, f);
+            const int c = column(v, lead);
+            if (EDGES) store_some<G, W>(to, c, dim, f);
+            else if (c < dim) store_vec<Cache::STREAM, G, W>(to + c, f);
         }
     }
-    __device__ float* partial(int64_t slot) const {
-        return k.partials + slot * k.dim_padded + col + lane * W;
-    }
+    // partial rows begin with the lead
+    __device__ float* partial(int64_t slot) const { return k.partials + slot * k.dim_padded; }
+    __device__ bool inside(int v) const { return column(v, lead) < dim; }
     // Keep the sum of a run that crosses the piece's bounds.
     __device__ void leave_partial(int64_t piece, bool from_before) {
         float* to = partial(2 * piece + (from_before ? 0 : 1));
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (inside(v)) store_vec<Cache::KEEP, float, W>(to + v * 32 * W, acc[v]);
+            if (inside(v)) store_vec<Cache::KEEP, float, W>(to + column(v, 0), acc[v]);
     }
     // This piece's part of the run of `id` is kept: the last piece to come here
     // adds the parts in piece order.
@@ -284,52 +357,89 @@ struct GradSum {
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before != last - first) return;
         __threadfence();
-        clear();
+        begin(id);
         for (int64_t q = first; q <= last; q += 4) {
             float got[4][V][W];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t part = min(q + u, last);
+                const float* from = partial(2 * part + (part == first ? 1 : 0));
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        got[u][v][i] = __ldcg(from + (inside(v) ? column(v, 0) : 0) + i);
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int i = 0; i < W; ++i)
-                        got[u][v][i] = q + u <= last && inside(v)
-                                           ? __ldcg(partial(2 * (q + u) + (q + u == first ? 1 : 0)) +
-                                                    v * 32 * W + i)
-                                           : 0.0f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int i = 0; i < W; ++i) acc[v][i] += got[u][v][i];
+                        if (q + u <= last) acc[v][i] += got[u][v][i];
         }
         finish(id);
     }
 
     __device__ void sum(int64_t piece, int panel) {
-        const T* dout = static_cast<const T*>(p.dout) + col + lane * W;
+        const T* dout = static_cast<const T*>(p.dout);
+        const int64_t elements = (p.tokens - 1) * p.ld_dout + p.dim;
         const int s0 = (int)(piece * k.piece);
         const int s1 = (int)min((int64_t)s0 + k.piece, p.tokens);
         unsigned run = (unsigned)(k.keys[s0] >> 32);            // the id being summed
         if (run == NO_ID) return;
         bool from_before = s0 > 0 && (unsigned)(k.keys[s0 - 1] >> 32) == run;
         unsigned head = NO_ID;                                  // a run from before that ended
-        clear();
+        begin(run);
         for (int base = s0; base < s1; base += 32) {
-            const uint64_t mine = base + lane < s1 ? k.keys[base + lane] : ~0ull;
-            const unsigned id_l = (unsigned)(mine >> 32), pos_l = (unsigned)mine;
+            const uint64_t mine = k.keys[min(base + lane, s1 - 1)];
+            const unsigned pos_l = (unsigned)mine;
+            const unsigned id_l = base + lane < s1 ? (unsigned)(mine >> 32) : NO_ID;
             const int live = __popc(__ballot_sync(0xffffffffu, id_l != NO_ID));  // a prefix
             for (int j = 0; j < live; j += BATCH) {
-                Vec<T, W> x[BATCH][V];
+                // all of a batch's rows at once; past the live ones and past the row some
+                // element is read in vain
+                using Read = std::conditional_t<EDGES, Unaligned<T>, Vec<T, W>>;
+                Read x[BATCH][V];
+                int64_t row[BATCH];
+                int leads[BATCH];
+                bool clear = true;
 #pragma unroll
                 for (int u = 0; u < BATCH; ++u) {
-                    const int64_t row = __shfl_sync(0xffffffffu, pos_l, (j + u) & 31);
+                    const int from = min(j + u, live - 1);
+                    row[u] = __shfl_sync(0xffffffffu, pos_l, from) * p.ld_dout;
+                    if constexpr (EDGES) {
+                        leads[u] = lead_for(__shfl_sync(0xffffffffu, id_l, from));
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (j + u < live && inside(v))
-                            x[u][v] = load_vec<Cache::STREAM, T, W>(dout + row * p.ld_dout +
-                                                                    v * 32 * W);
+                        for (int v = 0; v < V; ++v)
+                            clear &= clear_of_ends<W>(row[u] + min(column(v, leads[u]), dim - 1),
+                                                      elements);
+                    }
+                }
+                if constexpr (EDGES) {
+                    if (clear) {
+#pragma unroll
+                        for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+                            for (int v = 0; v < V; ++v)
+                                x[u][v].load(dout + row[u] + min(column(v, leads[u]), dim - 1));
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+                            for (int v = 0; v < V; ++v) {
+                                x[u][v].a = load_some<T, W>(dout + row[u], column(v, leads[u]), dim);
+                                x[u][v].b = x[u][v].a;
+                                x[u][v].shift = 0;
+                            }
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            x[u][v] = load_vec<Cache::STREAM, T, W>(
+                                dout + row[u] + (column(v, 0) < dim ? column(v, 0) : 0));
                 }
 #pragma unroll
                 for (int u = 0; u < BATCH; ++u) {
@@ -343,13 +453,14 @@ struct GradSum {
                         } else {
                             finish(run);
                         }
-                        clear();
+                        begin(id);
                         run = id;
                     }
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         float f[W];
-                        unpack(x[u][v], f);
+                        if constexpr (EDGES) unpack(x[u][v].get(), f);
+                        else unpack(x[u][v], f);
 #pragma unroll
                         for (int i = 0; i < W; ++i) acc[v][i] += f[i];
                     }
@@ -367,7 +478,7 @@ struct GradSum {
 };
 
 // Rows without a token: beta * dtable, zeros for beta == 0.
-template <typename G, int W>
+template <typename G, int W, bool EDGES>
 __device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t item, int lane) {
     const int64_t v0 = item * k.fill_rows;
     const int rows = (int)min((int64_t)k.fill_rows, p.vocab - v0);
@@ -391,32 +502,37 @@ __device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t i
     for (int r = 0; r < rows; ++r) {
         if (!(todo >> r & 1)) continue;
         G* to = static_cast<G*>(p.dtable) + (v0 + r) * p.ld_dtable;
-        for (int64_t c = lane * W; c < p.dim; c += 32 * W) {
+        const int dim = (int)p.dim;
+        for (int c = lane * W - (EDGES ? lead_of(to, 16) : 0); c < dim; c += 32 * W) {
             float f[W];
 #pragma unroll
             for (int i = 0; i < W; ++i) f[i] = 0.0f;
             if (p.beta != 0.0f) {
-                unpack(load_vec<Cache::STREAM, G, W>(to + c), f);
+                unpack(!EDGES || (c >= 0 && c + W <= dim) ? load_vec<Cache::STREAM, G, W>(to + c)
+                                                          : load_some<G, W>(to, c, dim), f);
 #pragma unroll
                 for (int i = 0; i < W; ++i) f[i] *= p.beta;
             }
-            store_vec<Cache::STREAM, G, W>(to + c, f);
+            if (EDGES) store_some<G, W>(to, c, dim, f);
+            else store_vec<Cache::STREAM, G, W>(to + c, f);
         }
     }
 }
 
-template <typename T, typename G, int W, int V, int BATCH>
+template <typename T, typename G, bool EDGES>
 __global__ __launch_bounds__(256) void grad_sums(EmbedGradParams p, GradWork k) {
+    constexpr int W = 16 / (int)sizeof(T), V = PANEL / 32 / W;
+    constexpr int BATCH = EDGES ? 4 / V : 8 / V;     // 8 words in flight per lane
     wait_for_predecessor();
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (item < k.sum_items) {
         const int panel = (int)(item % k.panels);
-        GradSum<T, G, W, V, BATCH> s{p, k, lane, (int64_t)panel * PANEL};
+        GradSum<T, G, W, V, BATCH, EDGES> s{p, k, lane, panel * PANEL, (int)p.dim};
         s.sum(item / k.panels, panel);
     } else {
         const int64_t fill = item - k.sum_items;
-        if (fill * k.fill_rows < p.vocab) fill_rows<G, W>(p, k, fill, lane);
+        if (fill * k.fill_rows < p.vocab) fill_rows<G, W, EDGES>(p, k, fill, lane);
     }
 }
 
@@ -430,7 +546,7 @@ GradLayout grad_layout(int64_t tokens, int64_t dim) {
     GradLayout l{};
     l.other = up((size_t)tokens * 8);
     l.arrived = l.other + up((size_t)tokens * 8);
-    l.partials = l.arrived + up(pieces * (size_t)panels_of(dim) * sizeof(int));
+    l.partials = l.arrived + up(pieces * (size_t)(panels_of(dim) + 1) * sizeof(int));
     l.total = l.partials + up(pieces * 2 * (size_t)padded(dim) * sizeof(float));
     return l;
 }
@@ -439,25 +555,20 @@ GradLayout grad_layout(int64_t tokens, int64_t dim) {
 
 cudaError_t launch_embedding(spmm_type_t type, const EmbedParams& p, int num_sms,
                              cudaStream_t st) {
-    return with_type(type, [&](auto t) {
-        using T = decltype(t);
-        constexpr int W = 16 / sizeof(T);
-        const bool wide = p.dim % W == 0 && rows_aligned16(p.out, p.ld_out, sizeof(T)) &&
-                          (p.vocab == 0 || rows_aligned16(p.table, p.ld_table, sizeof(T)));
-        return wide ? launch_embed<T, W>(p, num_sms, st) : launch_embed<T, 1>(p, num_sms, st);
-    });
+    return with_type(type, [&](auto t) { return launch_embed<decltype(t)>(p, num_sms, st); });
 }
 
 size_t embed_grad_scratch(int64_t tokens, int64_t dim) { return grad_layout(tokens, dim).total; }
 
 // Pieces get longer as the work grows, so a smaller call may need more: what
 // covers every call.  pieces <= min(tokens, SUM_WARPS / panels + 1), or
-// tokens / PIECE_MAX + 1 once the pieces are longest; padded(dim) <= PANEL * panels.
+// tokens / PIECE_MAX + 1 once the pieces are longest; padded(dim) <= PANEL * panels + 8.
 size_t embed_grad_scratch_upto(int64_t tokens, int64_t dim) {
     const size_t wide = (size_t)padded(dim), most = (size_t)tokens / PIECE_MAX + 1;
     const size_t rows = std::max(
-        std::min((size_t)tokens * wide, (size_t)SUM_WARPS * PANEL + wide), most * wide);
-    const size_t counters = std::max((size_t)SUM_WARPS + panels_of(dim), most * panels_of(dim));
+        std::min((size_t)tokens * wide, (size_t)SUM_WARPS * (PANEL + 8) + wide), most * wide);
+    const size_t panels = (size_t)panels_of(dim) + 1;
+    const size_t counters = std::max(2 * (size_t)SUM_WARPS + panels, most * panels);
     return (size_t)tokens * 16 + counters * sizeof(int) + rows * 2 * sizeof(float) + 4 * 256;
 }
 
@@ -473,7 +584,12 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
     k.partials = reinterpret_cast<float*>(scratch + l.partials);
     k.dim_padded = padded(p.dim);
     k.piece = piece_of(p.tokens, p.dim);
-    k.panels = (int)panels_of(p.dim);
+    const int W = 16 / lm_elem_size(type);
+    const bool whole = p.dim % W == 0 &&
+                       rows_aligned16(p.dtable, p.ld_dtable, lm_elem_size(grad_type)) &&
+                       (p.tokens == 0 || rows_aligned16(p.dout, p.ld_dout, lm_elem_size(type)));
+    // a row between boundaries covers up to W - 1 columns more
+    k.panels = (int)panels_of(p.dim + (whole ? 0 : W - 1));
     k.sum_items = (p.tokens + k.piece - 1) / k.piece * k.panels;
     // a filling warp writes about 32 KB when no row of its share has a token
     const int64_t row_bytes = p.dim * lm_elem_size(grad_type);
@@ -487,7 +603,7 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
         cudaError_t e = cudaGetLastError();
         for (int64_t run = SORT_TILE; e == cudaSuccess && run < p.tokens; run *= MERGE_WAYS) {
             e = launch_chained(merge_runs, dim3((unsigned)((p.tokens + 255) / 256)), dim3(256), 0,
-                               st, true, (const uint64_t*)keys, other, (int)p.tokens, run);
+                               st, true, (const uint64_t*)keys, other, (int)p.tokens, (int)run);
             std::swap(keys, other);
         }
         if (e != cudaSuccess) return e;
@@ -498,19 +614,12 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
     const bool same = type == grad_type;
     return with_type(type, [&](auto t) {
         using T = decltype(t);
-        constexpr int W = 16 / sizeof(T);
         auto run = [&](auto kernel) {
             return launch_chained(kernel, dim3((unsigned)blocks), dim3(256), 0, st, p.tokens > 0,
                                   p, k);
         };
-        const bool wide = p.dim % W == 0 &&
-                          rows_aligned16(p.dtable, p.ld_dtable, lm_elem_size(grad_type)) &&
-                          (p.tokens == 0 || rows_aligned16(p.dout, p.ld_dout, sizeof(T)));
-        if (same)
-            return wide ? run(grad_sums<T, T, W, PANEL / 32 / W, W>)
-                        : run(grad_sums<T, T, 1, PANEL / 32, 4>);
-        return wide ? run(grad_sums<T, float, W, PANEL / 32 / W, W>)
-                    : run(grad_sums<T, float, 1, PANEL / 32, 4>);
+        if (same) return whole ? run(grad_sums<T, T, false>) : run(grad_sums<T, T, true>);
+        return whole ? run(grad_sums<T, float, false>) : run(grad_sums<T, float, true>);
     });
 }
 

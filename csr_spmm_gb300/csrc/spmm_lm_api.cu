@@ -13,9 +13,9 @@ using namespace spmm;
 
 namespace {
 
-constexpr int64_t MAX_COUNT = INT_MAX - 1;      // rows, tokens and columns: 32-bit indices
+constexpr int64_t MAX_COUNT = INT_MAX - 1;      // rows, tokens, ids: 32-bit indices
 constexpr int64_t MAX_TOKENS = 1LL << 30;       // sorted tokens: room for padding in 32 bits
-constexpr int64_t MAX_WIDTH = 1LL << 30;        // columns of a layer norm, likewise
+constexpr int64_t MAX_WIDTH = 1LL << 30;        // columns, likewise
 
 inline bool bad_type(spmm_type_t t) { return t != SPMM_F32 && t != SPMM_F16 && t != SPMM_BF16; }
 // Parameters and gradients have the operands' type or binary32.
@@ -36,7 +36,7 @@ inline spmm_status_t launched(cudaError_t e) {
 extern "C" {
 
 spmm_status_t spmm_reserve_lm(spmm_handle_t h, int64_t rows, int64_t dim) {
-    if (!h || bad_count(rows, MAX_TOKENS) || bad_count(dim, MAX_COUNT))
+    if (!h || bad_count(rows, MAX_TOKENS) || bad_count(dim, MAX_WIDTH))
         return SPMM_ERR_INVALID_ARGUMENT;
     int sms = 0;
     spmm_status_t s = lm_device(h, &sms);
@@ -50,7 +50,7 @@ spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale, con
                              int64_t tokens, const void* table, int64_t ld_table, int64_t vocab,
                              int64_t dim, void* out, int64_t ld_out, void* stream) {
     if (!h || bad_type(type) || bad_count(tokens, MAX_COUNT) || bad_count(vocab, MAX_COUNT) ||
-        bad_count(dim, MAX_COUNT))
+        bad_count(dim, MAX_WIDTH))
         return SPMM_ERR_INVALID_ARGUMENT;
     if (short_ld(ld_table, dim) || short_ld(ld_out, dim)) return SPMM_ERR_DIMENSION_MISMATCH;
     if (tokens == 0 || dim == 0) return SPMM_OK;
@@ -68,7 +68,7 @@ spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t
                                   const void* dout, int64_t ld_dout, float beta, void* dtable,
                                   int64_t ld_dtable, int64_t vocab, int64_t dim, void* stream) {
     if (!h || bad_pair(type, grad_type) || bad_count(tokens, MAX_TOKENS) ||
-        bad_count(vocab, MAX_COUNT) || bad_count(dim, MAX_COUNT))
+        bad_count(vocab, MAX_COUNT) || bad_count(dim, MAX_WIDTH))
         return SPMM_ERR_INVALID_ARGUMENT;
     if (short_ld(ld_dout, dim) || short_ld(ld_dtable, dim)) return SPMM_ERR_DIMENSION_MISMATCH;
     if (vocab == 0 || dim == 0) return SPMM_OK;

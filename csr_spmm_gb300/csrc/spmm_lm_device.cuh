@@ -129,6 +129,80 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[W]) {
     }
 }
 
+// 16 bytes of elements from any element address: the two aligned words they lie in
+// (one, when aligned), and the bytes of the first that come before them.
+template <typename T>
+struct Unaligned {
+    static constexpr int W = 16 / (int)sizeof(T);
+    Vec<T, W> a, b;
+    unsigned shift;
+
+    __device__ __forceinline__ void load(const T* p) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        shift = at % 16;
+        const T* from = reinterpret_cast<const T*>(at - shift);
+        a = load_vec<Cache::KEEP, T, W>(from);
+        b = load_vec<Cache::KEEP, T, W>(from + (shift ? W : 0));
+    }
+    __device__ __forceinline__ Vec<T, W> get() const {
+        const uint32_t w[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
+        uint32_t t[6], u[5];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) t[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) u[i] = shift & 4 ? t[i + 1] : t[i];
+        Vec<T, W> r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(u[i], u[i + 1], (shift & 2) * 8);
+        return r;
+    }
+};
+// A matrix whose rows are read so: whether W elements from element `at` of the matrix
+// (rows and gaps) can be, i.e. no aligned word of theirs reaches over its ends.
+template <int W>
+__device__ __forceinline__ bool clear_of_ends(int64_t at, int64_t elements) {
+    return at >= W && at + 2 * W <= elements;
+}
+
+// Elements [c, c + W) of a row of `dim`, those outside it 0, one by one.
+template <typename T, int W>
+__device__ __forceinline__ Vec<T, W> load_some(const T* row, int c, int dim) {
+    Vec<T, W> r;
+    if constexpr (W == 1) {
+        r.w = c >= 0 && c < dim ? row[c] : from_f32<T>(0.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Vec<T, W>::WORDS; ++i) r.w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (c + i < 0 || c + i >= dim) continue;
+            if constexpr (sizeof(T) == 4)
+                r.w[i] = reinterpret_cast<const uint32_t*>(row)[c + i];
+            else
+                r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c + i]
+                              << ((i & 1) * 16);
+        }
+    }
+    return r;
+}
+// Stores W elements to [c, c + W) of a row of `dim`, a whole access at once (it must be
+// aligned then), those of another that lie in the row one by one.
+template <typename T, int W>
+__device__ __forceinline__ void store_some(T* row, int c, int dim, const float (&f)[W]) {
+    if (c >= 0 && c + W <= dim) {
+        store_vec<Cache::STREAM, T, W>(row + c, f);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        if (c + i >= 0 && c + i < dim) row[c + i] = from_f32<T>(f[i]);
+}
+// Columns before the row's start that its first aligned access of `bytes` covers.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T* row, int bytes) {
+    return (int)(reinterpret_cast<uintptr_t>(row) % bytes / sizeof(T));
+}
+
 // Asynchronous copies of a Vec into the issuing thread's own slot of shared
 // memory: no registers wait for them, and since no other thread reads the slot,
 // no barrier is needed either.  4 or 16 bytes (single 16-bit elements have none).

@@ -208,11 +208,23 @@ __device__ void collect(RowShared& sh, const Row<T>& row, const Part& part, int 
     for (int i0 = threadIdx.x; i0 < all; i0 += 4 * blockDim.x) {
         Vec<T, W> v[4];
         int64_t j[4];
+        bool all_whole = true;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int i = i0 + b * blockDim.x;
             j[b] = i < all ? part.access(sh.chosen[i / own], i % own) : -1;
-            if (j[b] >= 0) v[b] = row.template load<Cache::KEEP>(j[b]);
+            all_whole &= j[b] < 0 || row.whole(j[b]);
+        }
+        // an access behind a branch would keep the others waiting: those past the end are
+        // read in vain
+        if (all_whole && row.whole(1)) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                v[b] = load_vec<Cache::KEEP, T, W>(row.from + (j[b] < 0 ? 1 : j[b]) * W);
+        } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (j[b] >= 0) v[b] = row.template load<Cache::KEEP>(j[b]);
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {

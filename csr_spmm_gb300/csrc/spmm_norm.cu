@@ -42,27 +42,6 @@ __device__ __forceinline__ void row_barrier(int row, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "r"(threads) : "memory");
 }
 
-// Elements [c, c + W) of a row of `dim`, those outside it 0.
-template <typename T, int W>
-__device__ __forceinline__ Vec<T, W> load_some(const T* row, int c, int dim) {
-    Vec<T, W> r;
-    if constexpr (W == 1) {
-        r.w = c >= 0 && c < dim ? row[c] : from_f32<T>(0.0f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < Vec<T, W>::WORDS; ++i) r.w[i] = 0;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (c + i < 0 || c + i >= dim) continue;
-            if constexpr (sizeof(T) == 4)
-                r.w[i] = reinterpret_cast<const uint32_t*>(row)[c + i];
-            else
-                r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c + i]
-                              << ((i & 1) * 16);
-        }
-    }
-    return r;
-}
 // Parameters of columns [c, c + W), `none` where there are none.
 template <typename P, int W>
 __device__ __forceinline__ Vec<P, W> load_params(const void* p, int c, int dim, float none) {
@@ -142,16 +121,6 @@ __device__ __forceinline__ Vec<T, W> masked(Vec<T, W> v, const Vec<T, W>& mask, 
     for (int i = 0; i < Vec<T, W>::WORDS; ++i) v.w[i] &= mask.w[i] & all;
     return v;
 }
-template <typename T, int W>
-__device__ __forceinline__ void store_some(T* row, int c, int dim, const float (&f)[W]) {
-    if (c >= 0 && c + W <= dim) {
-        store_vec<Cache::STREAM, T, W>(row + c, f);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-        if (c + i >= 0 && c + i < dim) row[c + i] = from_f32<T>(f[i]);
-}
 template <int W>
 __device__ __forceinline__ void clear_outside(int c, int dim, float (&f)[W]) {
     if (c >= 0 && c + W <= dim) return;
@@ -159,12 +128,6 @@ __device__ __forceinline__ void clear_outside(int c, int dim, float (&f)[W]) {
     for (int i = 0; i < W; ++i)
         if (c + i < 0 || c + i >= dim) f[i] = 0.0f;
 }
-// Columns before the row's start that its first access covers.
-template <typename T, int W>
-__device__ __forceinline__ int lead_of(const T* row) {
-    return (int)(reinterpret_cast<uintptr_t>(row) % (W * sizeof(T)) / sizeof(T));
-}
-
 // ---- forward ------------------------------------------------------------------------
 
 // How a row meets its threads' accesses: ALL: every lane's are whole and in the row, and
@@ -203,7 +166,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
     }
     // the rows' first accesses begin `lead` columns before them; element i of access j is
     // column j W + i - lead
-    const int lead = EDGES ? lead_of<T, W>(x.row(r)) : 0;
+    const int lead = EDGES ? lead_of(x.row(r), W * (int)sizeof(T)) : 0;
     int param_at[EDGES ? W : 1];
 #pragma unroll
     for (int i = 0; i < (EDGES ? W : 0); ++i) {
@@ -222,11 +185,17 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
         if (EDGES && x.at_ends(r, p.rows)) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (in(k)) held[k] = x.load(row, c0 + k * step);
+                if (in(k)) held[k] = x.load(row, c0 + k * step);   // at_ends: !live too
         } else {
+            // past the row its last access is read in vain: one behind a branch would keep
+            // the others waiting
+            const T* from = live ? row : x.base;
+            const int last = (dim - 1 + lead) / W * W - lead;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (in(k)) held[k] = load_vec<Cache::STREAM, T, W>(row + c0 + k * step);
+            for (int k = 0; k < K; ++k) {
+                const int c = c0 + k * step;
+                held[k] = load_vec<Cache::STREAM, T, W>(from + (FIT == Fit::ALL ? c : min(c, last)));
+            }
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -406,7 +375,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
     const int slice = blockIdx.x * l.rows + in_block;
     int64_t r = slice, first = r - lane / l.lanes;
     // the tile's accesses follow the ones of the tiles before, so none is in two tiles
-    const int c0 = tid * W - (EDGES ? lead_of<T, W>(x.row(r)) : 0) + (GIVEN ? (int)blockIdx.y * GRAD_COLUMNS : 0);
+    const int c0 = tid * W - (EDGES ? lead_of(x.row(r), W * (int)sizeof(T)) : 0) + (GIVEN ? (int)blockIdx.y * GRAD_COLUMNS : 0);
     const int step = threads * W;
     auto in = [&](int k) { return FIT == Fit::ALL || c0 + k * step < dim; };
     auto fetch = [&](int64_t row, int stage) {
@@ -615,7 +584,7 @@ __global__ __launch_bounds__(ANY_THREADS) void grad_means(NormGradParams p) {
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const T* xr = x.row(r);
         const T* dyr = dy.row(r);
-        const int lead = W > 1 ? lead_of<T, W>(xr) : 0;
+        const int lead = W > 1 ? lead_of(xr, W * (int)sizeof(T)) : 0;
         const float mean = p.mean[r], rstd = p.rstd[r];
         float a = 0.0f, b = 0.0f;
         for (int c = threadIdx.x * W - lead; c < dim; c += 2 * ANY_THREADS * W) {
