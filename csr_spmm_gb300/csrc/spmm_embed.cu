@@ -124,8 +124,9 @@ cudaError_t launch_embed(const EmbedParams& p, int num_sms, cudaStream_t st) {
 // ---- gradient: sort ------------------------------------------------------------
 
 constexpr int SORT_TILE = 512;       // keys sorted by one block, one per thread
-constexpr int MERGE_WAYS = 16;       // sorted runs merged per round
-constexpr unsigned NO_ID = 0xfffffffeu;  // of padding; one more is still a number
+constexpr int MERGE_WAYS = 16;       // sorted runs merged per round, at most
+constexpr unsigned NO_ID = 0xfffffffdu;  // of padding tokens
+constexpr unsigned REST = 0xfffffffeu;   // behind them, what fills the last tile
 
 // Sorts each tile of SORT_TILE tokens with a bitonic network, one 64-bit key per
 // thread: exchanges within a warp are shuffles (35 of the 45 steps), the others
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(SORT_TILE) void sort_tiles(const int* ids, int toke
     allow_successor();
     const int t = threadIdx.x;
     const int64_t at = (int64_t)blockIdx.x * SORT_TILE + t;
-    uint64_t key = ~0ull;
+    uint64_t key = (uint64_t)REST << 32;
     if (at < tokens) {
         const int id = ids[at];
         key = (uint64_t)(id >= 0 && id < vocab ? (unsigned)id : NO_ID) << 32 | (unsigned)at;
@@ -164,7 +165,8 @@ __global__ __launch_bounds__(SORT_TILE) void sort_tiles(const int* ids, int toke
             key = (up == low) == (key < other) ? key : other;
         }
     }
-    if (at < tokens) keys[at] = key;
+    keys[at] = key;
+    if (at == 0) keys[(int64_t)gridDim.x * SORT_TILE] = ~0ull;
 }
 
 // Number of keys below `key` in a[0..n).
@@ -182,45 +184,46 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
     return lo;
 }
 
-// Merges groups of MERGE_WAYS sorted runs of `run` keys (a power of two): each key's
-// place is the count of smaller keys over the group's runs.  An earlier run holds
-// earlier tokens, so of equal ids those of earlier runs count, and the ids alone
-// decide.  The searches of all runs take their steps together, MERGE_WAYS loads
-// at a time and none behind a branch: a step costs one latency, not one for each run.
+// Merges groups of WAYS sorted runs of `run` keys (a power of two): each key's place
+// is the count of smaller keys over the group's runs.  An earlier run holds earlier
+// tokens, so of equal ids those of earlier runs count, and the ids alone decide.  The
+// searches of all runs take their steps together, WAYS loads at a time and none
+// behind a branch (hence no && on what they give): a step costs one latency, not one
+// for each run (8192 keys: 25 us when it did).  Behind the `total` keys (whole tiles)
+// lies a largest one, which ends every search that would go further.
+template <int WAYS>
 __global__ __launch_bounds__(256) void merge_runs(const uint64_t* __restrict__ in,
-                                                  uint64_t* __restrict__ out, int tokens, int run) {
+                                                  uint64_t* __restrict__ out, unsigned total,
+                                                  unsigned run) {
     allow_successor();
     wait_for_predecessor();
-    const int g = blockIdx.x * 256 + threadIdx.x;
-    if (g >= tokens) return;
+    const unsigned g = blockIdx.x * 256 + threadIdx.x;       // total is a multiple of 256
+    if (g == 0) out[total] = ~0ull;
     const uint64_t key = in[g];
     const unsigned id = (unsigned)(key >> 32);
     const unsigned* ids = reinterpret_cast<const unsigned*>(in) + 1;     // of key i at 2 i
-    const int last = tokens - 1;
-    // tokens <= 2^30: every start that matters fits 31 bits
-    const int64_t first = g / ((int64_t)run * MERGE_WAYS) * run * MERGE_WAYS;
-    const int own = (int)((g - first) / run);
-    int start[MERGE_WAYS], below[MERGE_WAYS];
+    // total <= 2^30 and run < total: no sum of these reaches 2^32 before it is cut at total
+    const unsigned first = (unsigned)(g / ((uint64_t)run * WAYS) * ((uint64_t)run * WAYS));
+    const unsigned own = (g - first) / run;
+    unsigned below[WAYS];
 #pragma unroll
-    for (int q = 0; q < MERGE_WAYS; ++q)
-        start[q] = below[q] = (int)min(first + (int64_t)q * run, (int64_t)tokens);
-    for (int half = run >> 1; half > 0; half >>= 1) {
-        unsigned got[MERGE_WAYS];
+    for (unsigned q = 0; q < WAYS; ++q) below[q] = (unsigned)min(first + (uint64_t)q * run, (uint64_t)total);
+    for (unsigned half = run >> 1; half > 0; half >>= 1) {
+        unsigned got[WAYS];
 #pragma unroll
-        for (int q = 0; q < MERGE_WAYS; ++q) got[q] = __ldg(ids + 2 * (int64_t)min(below[q] + half - 1, last));
+        for (unsigned q = 0; q < WAYS; ++q) got[q] = __ldg(ids + 2 * min(below[q] + half - 1, total));
 #pragma unroll
-        for (int q = 0; q < MERGE_WAYS; ++q)
-            if (below[q] + half - 1 <= last && got[q] < id + (q < own)) below[q] += half;
+        for (unsigned q = 0; q < WAYS; ++q) below[q] += got[q] < id + (q < own) ? half : 0;
     }
     // one candidate is left in each run
-    unsigned got[MERGE_WAYS];
-    int place = (int)first;
+    unsigned got[WAYS], place = first;
 #pragma unroll
-    for (int q = 0; q < MERGE_WAYS; ++q) got[q] = __ldg(ids + 2 * (int64_t)min(below[q], last));
+    for (unsigned q = 0; q < WAYS; ++q) got[q] = __ldg(ids + 2 * min(below[q], total));
 #pragma unroll
-    for (int q = 0; q < MERGE_WAYS; ++q)
-        place += q == own ? g - start[q]
-                          : below[q] - start[q] + (below[q] <= last && got[q] < id + (q < own));
+    for (unsigned q = 0; q < WAYS; ++q) {
+        const unsigned start = (unsigned)min(first + (uint64_t)q * run, (uint64_t)total);
+        place += q == own ? g - start : below[q] - start + (got[q] < id + (q < own));
+    }
     out[place] = key;
 }
 
@@ -229,11 +232,15 @@ __global__ __launch_bounds__(256) void merge_runs(const uint64_t* __restrict__ i
 // The sorted tokens are cut into pieces of equal length; a warp sums one piece
 // over one panel of columns, reading each token's row segment once.  A run of
 // one id that lies within the piece is complete and goes to its table row; a
-// run that crosses the piece's bounds leaves a partial sum, and the last of the
-// run's pieces to arrive adds the run's partials in piece order.
+// run that crosses the piece's bounds leaves a partial sum.  Of each JOIN pieces
+// (by number) the last one to arrive adds the run's partials in piece order, and
+// the last of those sums to arrive adds them in order: a token that makes up a
+// tenth of 300,000 has near a thousand pieces.
 constexpr int PANEL = 256;           // columns per warp: 512 bytes of a 16-bit row
 constexpr int PIECE_MAX = 256;
-constexpr int64_t SUM_WARPS = 16384;
+constexpr int64_t SUM_WARPS = 8192;
+constexpr int JOIN = 32;             // pieces of a run joined at once
+constexpr int COUNTERS = 3;          // per piece and panel
 
 // Tokens per piece: as many as leave about SUM_WARPS warps of work (three to four
 // times what the SMs hold at once), so that few runs are cut; one where there is
@@ -251,7 +258,7 @@ inline int64_t padded(int64_t dim) { return (dim + 7) / 8 * 8 + 8; }
 struct GradWork {
     const uint64_t* keys;            // sorted
     float* partials;                 // [pieces][2][padded dim]: run from before, run to the next
-    int* arrived;                    // [pieces][panels], zeroed by sort_tiles
+    int* arrived;                    // [COUNTERS][pieces][panels], zeroed by sort_tiles
     int64_t dim_padded;
     int piece;
     int panels;
@@ -259,19 +266,41 @@ struct GradWork {
     int fill_rows;                   // table rows per filling warp
 };
 
-// Number of keys below `key`, by the whole warp: 32 probes per step.
-__device__ __forceinline__ int warp_count_below(const uint64_t* a, int n, uint64_t key, int lane) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int step = (hi - lo) / 32 + 1;
-        const int64_t at = lo + (int64_t)lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, at < hi && a[at] < key);
-        const int k = __popc(below);
-        if (k == 0) return lo;
-        hi = (int)min((int64_t)hi, lo + (int64_t)k * step);
-        lo += (k - 1) * step + 1;
+// Number of keys below each of `key`, by the whole warp: 32 probes per key and step.
+template <int N>
+__device__ __forceinline__ void warp_count_below(const uint64_t* a, int n, const uint64_t (&key)[N],
+                                                 int (&count)[N], int lane) {
+    int lo[N], hi[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        lo[i] = 0;
+        hi[i] = n;
     }
-    return lo;
+    bool open = n > 0;
+    while (open) {
+        uint64_t got[N];
+        int step[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            step[i] = (hi[i] - lo[i]) / 32 + 1;
+            got[i] = a[min((int64_t)lo[i] + (int64_t)lane * step[i], (int64_t)n - 1)];
+        }
+        open = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool is = (int64_t)lo[i] + (int64_t)lane * step[i] < hi[i];
+            const int k = __popc(__ballot_sync(0xffffffffu, is & (got[i] < key[i])));
+            if (k == 0) {
+                hi[i] = lo[i];
+            } else {
+                hi[i] = (int)min((int64_t)hi[i], lo[i] + (int64_t)k * step[i]);
+                lo[i] += (k - 1) * step[i] + 1;
+            }
+            open |= lo[i] < hi[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) count[i] = lo[i];
 }
 
 // W elements per access, V accesses per lane and row segment: W * V * 32 == PANEL.
@@ -343,40 +372,73 @@ struct GradSum {
         for (int v = 0; v < V; ++v)
             if (inside(v)) store_vec<Cache::KEEP, float, W>(to + column(v, 0), acc[v]);
     }
-    // This piece's part of the run of `id` is kept: the last piece to come here
-    // adds the parts in piece order.
-    __device__ void join(unsigned id, int panel) {
-        const int n = (int)p.tokens;
-        const int a = warp_count_below(k.keys, n, (uint64_t)id << 32, lane);
-        const int b = warp_count_below(k.keys, n, (uint64_t)(id + 1) << 32, lane);
-        const int64_t first = a / k.piece, last = (b - 1) / k.piece;
+    // Whether this warp is the last of `all` to come to a counter; what the others wrote
+    // before is visible then.
+    __device__ bool last_of(int64_t counter, int panel, int64_t all) const {
         __threadfence();
         __syncwarp();
         int before = 0;
-        if (lane == 0) before = atomicAdd(k.arrived + first * k.panels + panel, 1);
+        if (lane == 0) before = atomicAdd(k.arrived + counter * k.panels + panel, 1);
         before = __shfl_sync(0xffffffffu, before, 0);
-        if (before != last - first) return;
         __threadfence();
-        begin(id);
-        for (int64_t q = first; q <= last; q += 4) {
-            float got[4][V][W];
+        return before == all - 1;
+    }
+    // Adds the partials of every `stride`-th piece from `from` to `to`; of the run's first
+    // piece `first` it is the second one.
+    __device__ void add_partials(int64_t from, int64_t to, int64_t stride, int64_t first) {
+        constexpr int MANY = 8;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t part = min(q + u, last);
-                const float* from = partial(2 * part + (part == first ? 1 : 0));
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[v][i] = 0.0f;
+        for (int64_t q = from; q <= to; q += MANY * stride) {
+            float got[MANY][V][W];
+#pragma unroll
+            for (int u = 0; u < MANY; ++u) {
+                const int64_t piece = q + u * stride <= to ? q + u * stride : q;
+                const float* part = partial(2 * piece + (piece == first));
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int i = 0; i < W; ++i)
-                        got[u][v][i] = __ldcg(from + (inside(v) ? column(v, 0) : 0) + i);
+                        got[u][v][i] = __ldcg(part + (inside(v) ? column(v, 0) : 0) + i);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < MANY; ++u)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int i = 0; i < W; ++i)
-                        if (q + u <= last) acc[v][i] += got[u][v][i];
+                        acc[v][i] += q + u * stride <= to ? got[u][v][i] : 0.0f;
+        }
+    }
+    // This piece's part of the run of `id` is kept: the last to come here joins the parts.
+    __device__ void join(int64_t piece, unsigned id, int panel) {
+        const uint64_t bounds[2] = {(uint64_t)id << 32, (uint64_t)(id + 1) << 32};
+        int at[2];
+        warp_count_below(k.keys, (int)p.tokens, bounds, at, lane);
+        const int64_t first = at[0] / k.piece, last = (at[1] - 1) / k.piece;
+        const int64_t from = max(first, piece / JOIN * JOIN);
+        const int64_t to = min(last, piece / JOIN * JOIN + JOIN - 1);
+        const int64_t pieces = k.sum_items / k.panels;
+        // a piece begins one run and may continue another: two counters
+        if (!last_of((from == first ? pieces : 0) + from, panel, to - from + 1)) return;
+        lead = lead_for(id);
+        add_partials(from, to, 1, first);
+        if (first / JOIN != last / JOIN) {
+            float* sum = partial(2 * from + (from == first));
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (inside(v)) store_vec<Cache::KEEP, float, W>(sum + column(v, 0), acc[v]);
+            if (!last_of(2 * pieces + first, panel, last / JOIN - first / JOIN + 1)) return;
+            // the first group's sum is at `first`, the others' at their first pieces
+            add_partials((first / JOIN + 1) * JOIN, last, JOIN, first);
+            const float* part = partial(2 * first + 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    acc[v][i] = __ldcg(part + (inside(v) ? column(v, 0) : 0) + i) + acc[v][i];
         }
         finish(id);
     }
@@ -472,13 +534,13 @@ struct GradSum {
         const bool crosses = from_before || goes_on;
         if (crosses) leave_partial(piece, from_before);
         else finish(run);
-        if (head != NO_ID) join(head, panel);
-        if (crosses) join(run, panel);
+        if (head != NO_ID) join(piece, head, panel);
+        if (crosses) join(piece, run, panel);
     }
 };
 
 // Rows without a token: beta * dtable, zeros for beta == 0.
-template <typename G, int W, bool EDGES>
+template <typename G, bool EDGES>
 __device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t item, int lane) {
     const int64_t v0 = item * k.fill_rows;
     const int rows = (int)min((int64_t)k.fill_rows, p.vocab - v0);
@@ -486,7 +548,10 @@ __device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t i
     const unsigned all = rows == 32 ? ~0u : (1u << rows) - 1;
     // where the first of these rows would be, and 32 keys from there: enough unless
     // its tokens are many, and then the other rows look for themselves
-    const int at = warp_count_below(k.keys, n, (uint64_t)v0 << 32, lane);
+    const uint64_t bound[1] = {(uint64_t)v0 << 32};
+    int found[1];
+    warp_count_below(k.keys, n, bound, found, lane);
+    const int at = found[0];
     const uint64_t key = at + lane < n ? k.keys[at + lane] : ~0ull;
     const int64_t row = (int64_t)(key >> 32) - v0;
     unsigned present = __reduce_or_sync(0xffffffffu, row < rows ? 1u << row : 0u);
@@ -501,6 +566,7 @@ __device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t i
     const unsigned todo = all & ~present;
     for (int r = 0; r < rows; ++r) {
         if (!(todo >> r & 1)) continue;
+        constexpr int W = 16 / (int)sizeof(G);
         G* to = static_cast<G*>(p.dtable) + (v0 + r) * p.ld_dtable;
         const int dim = (int)p.dim;
         for (int c = lane * W - (EDGES ? lead_of(to, 16) : 0); c < dim; c += 32 * W) {
@@ -532,8 +598,13 @@ __global__ __launch_bounds__(256) void grad_sums(EmbedGradParams p, GradWork k) 
         s.sum(item / k.panels, panel);
     } else {
         const int64_t fill = item - k.sum_items;
-        if (fill * k.fill_rows < p.vocab) fill_rows<G, W, EDGES>(p, k, fill, lane);
+        if (fill * k.fill_rows < p.vocab) fill_rows<G, EDGES>(p, k, fill, lane);
     }
+}
+
+// Whole tiles and the key behind them.
+size_t key_bytes(int64_t tokens) {
+    return (size_t)((tokens + SORT_TILE - 1) / SORT_TILE * SORT_TILE + 1) * sizeof(uint64_t);
 }
 
 struct GradLayout {
@@ -544,9 +615,9 @@ GradLayout grad_layout(int64_t tokens, int64_t dim) {
     const int piece = piece_of(tokens, dim);
     const size_t pieces = (size_t)((tokens + piece - 1) / piece);
     GradLayout l{};
-    l.other = up((size_t)tokens * 8);
-    l.arrived = l.other + up((size_t)tokens * 8);
-    l.partials = l.arrived + up(pieces * (size_t)(panels_of(dim) + 1) * sizeof(int));
+    l.other = up(key_bytes(tokens));
+    l.arrived = l.other + up(key_bytes(tokens));
+    l.partials = l.arrived + up(pieces * (size_t)(panels_of(dim) + 1) * COUNTERS * sizeof(int));
     l.total = l.partials + up(pieces * 2 * (size_t)padded(dim) * sizeof(float));
     return l;
 }
@@ -569,7 +640,8 @@ size_t embed_grad_scratch_upto(int64_t tokens, int64_t dim) {
         std::min((size_t)tokens * wide, (size_t)SUM_WARPS * (PANEL + 8) + wide), most * wide);
     const size_t panels = (size_t)panels_of(dim) + 1;
     const size_t counters = std::max(2 * (size_t)SUM_WARPS + panels, most * panels);
-    return (size_t)tokens * 16 + counters * sizeof(int) + rows * 2 * sizeof(float) + 4 * 256;
+    return 2 * key_bytes(tokens) + counters * COUNTERS * sizeof(int) +
+           rows * 2 * sizeof(float) + 4 * 256;
 }
 
 cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
@@ -599,12 +671,17 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
     if (p.tokens > 0) {
         const int tiles = (int)((p.tokens + SORT_TILE - 1) / SORT_TILE);
         sort_tiles<<<tiles, SORT_TILE, 0, st>>>(p.ids, (int)p.tokens, p.vocab, keys, k.arrived,
-                                                k.sum_items);
+                                                k.sum_items * COUNTERS);
         cudaError_t e = cudaGetLastError();
-        for (int64_t run = SORT_TILE; e == cudaSuccess && run < p.tokens; run *= MERGE_WAYS) {
-            e = launch_chained(merge_runs, dim3((unsigned)((p.tokens + 255) / 256)), dim3(256), 0,
-                               st, true, (const uint64_t*)keys, other, (int)p.tokens, (int)run);
+        const unsigned total = (unsigned)tiles * SORT_TILE;
+        for (int64_t run = SORT_TILE; e == cudaSuccess && run < total;) {
+            const int64_t runs = (total + run - 1) / run;
+            const int ways = runs <= 4 ? 4 : runs <= 8 ? 8 : MERGE_WAYS;
+            auto kernel = ways == 4 ? merge_runs<4> : ways == 8 ? merge_runs<8> : merge_runs<16>;
+            e = launch_chained(kernel, dim3(total / 256), dim3(256), 0, st, true,
+                               (const uint64_t*)keys, other, total, (unsigned)run);
             std::swap(keys, other);
+            run *= ways;
         }
         if (e != cudaSuccess) return e;
     }
