@@ -186,44 +186,44 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
 
 // Merges groups of WAYS sorted runs of `run` keys (a power of two): each key's place
 // is the count of smaller keys over the group's runs.  An earlier run holds earlier
-// tokens, so of equal ids those of earlier runs count, and the ids alone decide.  The
-// searches of all runs take their steps together, WAYS loads at a time and none
-// behind a branch (hence no && on what they give): a step costs one latency, not one
-// for each run (8192 keys: 25 us when it did).  Behind the `total` keys (whole tiles)
-// lies a largest one, which ends every search that would go further.
+// tokens, so of equal ids those of earlier runs count, and the ids alone decide.
+// A block takes 32 consecutive keys, a warp of it one of the runs: its lanes search
+// for neighbouring keys, so their probes share memory words, and a search is one chain
+// of loads with many others beside it (one thread per key with WAYS chains: 8192 keys
+// 25 us).  Behind the `total` keys (whole tiles) lies a largest one, which ends every
+// search that would go further.
 template <int WAYS>
-__global__ __launch_bounds__(256) void merge_runs(const uint64_t* __restrict__ in,
-                                                  uint64_t* __restrict__ out, unsigned total,
-                                                  unsigned run) {
+__global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restrict__ in,
+                                                        uint64_t* __restrict__ out,
+                                                        unsigned total, unsigned run) {
+    __shared__ unsigned count[WAYS][32];
     allow_successor();
     wait_for_predecessor();
-    const unsigned g = blockIdx.x * 256 + threadIdx.x;       // total is a multiple of 256
-    if (g == 0) out[total] = ~0ull;
+    const unsigned lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const unsigned g = blockIdx.x * 32 + lane;
+    if (g == 0 && q == 0) out[total] = ~0ull;
     const uint64_t key = in[g];
-    const unsigned id = (unsigned)(key >> 32);
     const unsigned* ids = reinterpret_cast<const unsigned*>(in) + 1;     // of key i at 2 i
     // total <= 2^30 and run < total: no sum of these reaches 2^32 before it is cut at total
-    const unsigned first = (unsigned)(g / ((uint64_t)run * WAYS) * ((uint64_t)run * WAYS));
+    const uint64_t group = (uint64_t)run * WAYS;
+    const unsigned first = (unsigned)(g / group * group);
     const unsigned own = (g - first) / run;
-    unsigned below[WAYS];
-#pragma unroll
-    for (unsigned q = 0; q < WAYS; ++q) below[q] = (unsigned)min(first + (uint64_t)q * run, (uint64_t)total);
-    for (unsigned half = run >> 1; half > 0; half >>= 1) {
-        unsigned got[WAYS];
-#pragma unroll
-        for (unsigned q = 0; q < WAYS; ++q) got[q] = __ldg(ids + 2 * min(below[q] + half - 1, total));
-#pragma unroll
-        for (unsigned q = 0; q < WAYS; ++q) below[q] += got[q] < id + (q < own) ? half : 0;
+    const unsigned start = (unsigned)min(first + (uint64_t)q * run, (uint64_t)total);
+    unsigned below = start;
+    if (q == own) {
+        below = g;
+    } else {
+        const unsigned bound = (unsigned)(key >> 32) + (q < own);
+        for (unsigned half = run >> 1; half > 0; half >>= 1)
+            below += __ldg(ids + 2 * min(below + half - 1, total)) < bound ? half : 0;
+        below += __ldg(ids + 2 * min(below, total)) < bound;    // one candidate is left
     }
-    // one candidate is left in each run
-    unsigned got[WAYS], place = first;
+    count[q][lane] = below - start;
+    __syncthreads();
+    if (q > 0) return;
+    unsigned place = first;
 #pragma unroll
-    for (unsigned q = 0; q < WAYS; ++q) got[q] = __ldg(ids + 2 * min(below[q], total));
-#pragma unroll
-    for (unsigned q = 0; q < WAYS; ++q) {
-        const unsigned start = (unsigned)min(first + (uint64_t)q * run, (uint64_t)total);
-        place += q == own ? g - start : below[q] - start + (got[q] < id + (q < own));
-    }
+    for (int i = 0; i < WAYS; ++i) place += count[i][lane];
     out[place] = key;
 }
 
@@ -678,7 +678,7 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
             const int64_t runs = (total + run - 1) / run;
             const int ways = runs <= 4 ? 4 : runs <= 8 ? 8 : MERGE_WAYS;
             auto kernel = ways == 4 ? merge_runs<4> : ways == 8 ? merge_runs<8> : merge_runs<16>;
-            e = launch_chained(kernel, dim3(total / 256), dim3(256), 0, st, true,
+            e = launch_chained(kernel, dim3(total / 32), dim3(32 * ways), 0, st, true,
                                (const uint64_t*)keys, other, total, (unsigned)run);
             std::swap(keys, other);
             run *= ways;
