@@ -215,7 +215,8 @@ SHAPES = [(1, 1, 0, 0), (3, 2, 0, 0), (5, 31, 0, 0), (130, 64, 0, 0), (4, 256, 8
           (1000, 128, 0, 0), (33, 1000, 0, 1), (70, 1001, 0, 0), (9, 2048, 0, 0),
           (513, 520, 16, 0), (40, 4096, 0, 0), (7, 5000, 3, 0), (12, 8192, 0, 0),
           (3, 8200, 0, 0), (5, 16384, 0, 0), (2, 20000, 0, 0), (2, 70001, 0, 0),
-          (1, 40960, 0, 0), (3000, 48, 0, 0)]
+          (1, 40960, 0, 0), (3000, 48, 0, 0), (4000, 7, 0, 0), (9000, 3, 0, 1), (2600, 515, 0, 0),
+          (1300, 2048, 0, 0), (700, 8200, 1, 0), (350, 16391, 0, 0), (2, 65536, 0, 0)]
 
 
 @pytest.mark.parametrize("t,pt", [("f32", "f32"), ("f16", "f16"), ("f16", "f32"),
@@ -352,9 +353,11 @@ def test_token_logprob(cs, handle, t, rows, vocab, k, alpha, pad, offset):
 
 
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("vocab", [5, 64, 300, 1001, 9000, 70000])
-def test_token_logprob_masks_and_special_values(cs, handle, t, vocab):
-    """Rows with masked, lowest, equal, infinite and NaN logits."""
+@pytest.mark.parametrize("vocab,times", [(5, 1), (64, 1), (300, 1), (1001, 1), (9000, 1),
+                                         (70000, 1), (1001, 60), (9003, 60), (40001, 60)])
+def test_token_logprob_masks_and_special_values(cs, handle, t, vocab, times):
+    """Rows with masked, lowest, equal, infinite and NaN logits: few rows, and the same
+    rows `times` over (every copy must give the same bits)."""
     rng = np.random.default_rng(vocab)
     x, _ = _make(rng, (14, vocab), t, 2.0)
     low = float(torch.finfo(DT[t]).min)
@@ -379,6 +382,26 @@ def test_token_logprob_masks_and_special_values(cs, handle, t, vocab):
     x[11] = float(torch.finfo(DT[t]).max)              # the largest value everywhere
     x[12] = torch.randint(0, 2, (vocab,), device="cuda").to(DT[t])   # two values: many ties
     x[13, ::3] = -inf
+    if times > 1:
+        many = x.repeat(times, 1)
+        targets = torch.full((14 * times,), last, dtype=torch.int32, device="cuda")
+        for k in (0, 4, 32):
+            got = cs.token_logprob(handle, many, targets, top=k)
+            ld = many.stride(0) * many.element_size()
+            for g in got:
+                g = g.view(times, 14, -1)
+                # copies that lie alike against 16-byte boundaries
+                step = 16 // np.gcd(16, 14 * ld)
+                want = g[:step].repeat(-(-times // step), 1, 1)[:times]
+                same = (g == want) | ((g != g) & (want != want))
+                assert bool(same.all())
+            first = [g[:14].double().cpu().numpy() for g in got]
+            want, tol = ref.token_logprob(_np(x), targets[:14].cpu().numpy(), 1.0)
+            for g, name in zip(first, ("logprob", "entropy", "lse")):
+                _near(g, want[name], tol[name], name)
+            if k:
+                assert np.array_equal(first[4], ref.top(_np(x), k))
+        return
     h_x = _np(x)
     for k in (0, 4, 32):
         targets = np.full(14, last, np.int32)
@@ -386,6 +409,24 @@ def test_token_logprob_masks_and_special_values(cs, handle, t, vocab):
         targets[:] = -1
         _check_logprob(cs, handle, x, h_x, targets, 0.5, k)
     _check_logprob(cs, handle, x, h_x, None, 1.0, 2)
+
+
+@pytest.mark.parametrize("rows", [2, 700])
+def test_token_logprob_alternatives_in_few_hands(cs, handle, rows):
+    """All that is not masked lies in the accesses of eight lanes, more of it than the
+    list of candidates holds; and the same above a floor of equal logits."""
+    vocab = 65536
+    at = torch.arange(vocab, device="cuda")
+    few = (at // 4 % 32 < 8) & (at // 128 % 32 < 4)
+    torch.manual_seed(3)
+    for low in (-float("inf"), -7.0):
+        x = torch.full((rows, vocab), low, device="cuda")
+        x[:, few] = torch.randn(rows, int(few.sum()), device="cuda")
+        assert int(few.sum()) > 1024
+        _, _, lse, lp, index = cs.token_logprob(handle, x, None, top=32)
+        want = torch.topk(x, 32, dim=1)
+        assert torch.equal(index.long(), want.indices)
+        assert torch.allclose(lp, want.values - lse[:, None], atol=1e-5)
 
 
 def test_token_logprob_empty(cs, handle):
