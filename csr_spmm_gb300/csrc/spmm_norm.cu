@@ -436,11 +436,11 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
         const float2 ab = next_ab;
         statistics(r + slices);
         copies_wait<STAGES - 2>();
-        uint64_t xh[K][W / 2], g[K][W / 2];
         uint64_t a2 = pair(0.0f, 0.0f), b2 = a2;
         const uint64_t m2 = pair(-mean, -mean), r2 = pair(rstd, rstd);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
+        // xhat, dy and dy * weight of access k.  Rows with edges take them from the ring for
+        // each of two passes: beside the masks there is no room to keep them.
+        auto take = [&](int k, uint64_t (&xh)[W / 2], uint64_t (&d)[W / 2], uint64_t (&g)[W / 2]) {
             float xf[W], gf[W], wf[W];
             const Vec<T, W>* from = ring + (stage * 2 * K + k) * blockDim.x;
             if constexpr (EDGES) {
@@ -454,19 +454,32 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
             unpack(w[k], wf);
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
-                const uint64_t d = pair(gf[2 * i], gf[2 * i + 1]);
-                xh[k][i] = mul2(add2(pair(xf[2 * i], xf[2 * i + 1]), m2), r2);
-                dw[k][i] = fma2(d, xh[k][i], dw[k][i]);
-                db[k][i] = add2(db[k][i], d);
-                g[k][i] = mul2(d, pair(wf[2 * i], wf[2 * i + 1]));
+                d[i] = pair(gf[2 * i], gf[2 * i + 1]);
+                xh[i] = mul2(add2(pair(xf[2 * i], xf[2 * i + 1]), m2), r2);
+                g[i] = mul2(d[i], pair(wf[2 * i], wf[2 * i + 1]));
+            }
+        };
+        uint64_t kept[EDGES ? 1 : 2][EDGES ? 1 : K][W / 2];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            uint64_t xh[W / 2], d[W / 2], g[W / 2];
+            take(k, xh, d, g);
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                if constexpr (!EDGES) {
+                    kept[0][k][i] = xh[i];
+                    kept[1][k][i] = g[i];
+                }
+                dw[k][i] = fma2(d[i], xh[i], dw[k][i]);
+                db[k][i] = add2(db[k][i], d[i]);
                 if (!GIVEN) {
-                    a2 = add2(a2, g[k][i]);
-                    b2 = fma2(g[k][i], xh[k][i], b2);
+                    a2 = add2(a2, g[i]);
+                    b2 = fma2(g[i], xh[i], b2);
                 }
             }
         }
+        // to the stage of the row before
         fetch(r + (int64_t)(STAGES - 1) * slices, stage == 0 ? STAGES - 1 : stage - 1);
-        stage = stage == STAGES - 1 ? 0 : stage + 1;
         float a, b;
         if constexpr (GIVEN) {
             a = ab.x;
@@ -493,20 +506,31 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
             a *= per_dim;
             b *= per_dim;
         }
-        if (!live) continue;
         T* dx = static_cast<T*>(p.dx) + r * p.ld_dx;
         const uint64_t na = pair(-a, -a), nb = pair(-b, -b);
+        if (live)
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = c0 + k * step;
-            if (!in(k)) continue;
-            float f[W];
+            for (int k = 0; k < K; ++k) {
+                const int c = c0 + k * step;
+                uint64_t xh[W / 2], d[W / 2], g[W / 2];
+                if constexpr (EDGES) {
+                    take(k, xh, d, g);
+                } else {
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i)
-                halves(mul2(r2, fma2(nb, xh[k][i], add2(g[k][i], na))), f[2 * i], f[2 * i + 1]);
-            if (EDGES) store_some<T, W>(dx, c, dim, f);
-            else store_vec<Cache::STREAM, T, W>(dx + c, f);
-        }
+                    for (int i = 0; i < W / 2; ++i) {
+                        xh[i] = kept[0][k][i];
+                        g[i] = kept[1][k][i];
+                    }
+                }
+                if (!in(k)) continue;
+                float f[W];
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i)
+                    halves(mul2(r2, fma2(nb, xh[i], add2(g[i], na))), f[2 * i], f[2 * i + 1]);
+                if (EDGES) store_some<T, W>(dx, c, dim, f);
+                else store_vec<Cache::STREAM, T, W>(dx + c, f);
+            }
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
     }
     allow_successor();
     if (!p.part) return;
