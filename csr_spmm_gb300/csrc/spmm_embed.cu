@@ -94,10 +94,18 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int n
         for (int u = 0; u < EMBED_BATCH; ++u) {
             if (row[u] >= rows) continue;
             const bool valid = id[u] >= 0 && id[u] < p.vocab;
-            float f[W];
-            unpack(EDGES ? far[EDGES ? u : 0].get() : v[u], f);
+            Vec<T, W> got = v[u];
+            if constexpr (EDGES) got = far[u].get();
+            // padding: zero bits, four at a time rather than element by element
+            const uint32_t keep = valid ? ~0u : 0u;
 #pragma unroll
-            for (int i = 0; i < W; ++i) f[i] = valid ? p.scale * f[i] : 0.0f;
+            for (int i = 0; i < Vec<T, W>::WORDS; ++i) got.w[i] &= keep;
+            const float scale = valid ? p.scale : 0.0f;
+            const uint64_t scale2 = pair(scale, scale);
+            float f[W];
+            unpack(got, f);
+#pragma unroll
+            for (int i = 0; i < W; i += 2) halves(mul2(pair(f[i], f[i + 1]), scale2), f[i], f[i + 1]);
             if (EDGES) store_some<T, W>(out + row[u] * p.ld_out, col[u], dim, f);
             else store_vec<Cache::STREAM, T, W>(out + row[u] * p.ld_out + col[u], f);
         }
