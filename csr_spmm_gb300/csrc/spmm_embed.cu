@@ -24,7 +24,9 @@ constexpr int EMBED_BATCH = 4;       // accesses in flight per thread
 // rows share a warp and the stores of neighbouring threads are contiguous.
 // EDGES: any width and alignment: accesses are those of out's aligned words, and
 // the table is read from wherever their elements lie.  The bound is HBM: one table
-// row read and one written per token.
+// row read and one written per token.  100,003 Zipf-distributed tokens of 4096 bf16:
+// 172 us, 6.1 TB/s of distinct rows read and rows written (90% of the copy rate; 241 us
+// before a batch's accesses were free of branches and kept packed).
 template <typename T, bool EDGES>
 __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int nv,
                                                             int block_rows) {
@@ -197,8 +199,8 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
 // tokens, so of equal ids those of earlier runs count, and the ids alone decide.
 // A block takes 32 consecutive keys, a warp of it one of the runs: its lanes search
 // for neighbouring keys, so their probes share memory words, and a search is one chain
-// of loads with many others beside it (one thread per key with WAYS chains: 8192 keys
-// 25 us).  Behind the `total` keys (whole tiles) lies a largest one, which ends every
+// of loads with many others beside it: 8192 keys 5 us (one thread per key with WAYS
+// chains: 25 us, its loads waiting for one another), 65,536 in two rounds 22 us.  Behind the `total` keys (whole tiles) lies a largest one, which ends every
 // search that would go further.
 template <int WAYS>
 __global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restrict__ in,
@@ -243,7 +245,10 @@ __global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restri
 // run that crosses the piece's bounds leaves a partial sum.  Of each JOIN pieces
 // (by number) the last one to arrive adds the run's partials in piece order, and
 // the last of those sums to arrive adds them in order: a token that makes up a
-// tenth of 300,000 has near a thousand pieces.
+// tenth of 300,000 has near a thousand pieces.  Warps behind those of the sums write the
+// rows without a token.  The bound is HBM: 65,536 tokens of 4096 bf16 into a table of
+// 131,072 binary32 rows take 414 us with the sort, 6.5 TB/s of what must move (95% of
+// the copy rate).
 constexpr int PANEL = 256;           // columns per warp: 512 bytes of a 16-bit row
 constexpr int PIECE_MAX = 256;
 constexpr int64_t SUM_WARPS = 8192;

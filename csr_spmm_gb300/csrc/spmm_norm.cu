@@ -6,7 +6,7 @@
 // sum (x - m)^2 = sum_w [sum (x - m_w)^2 + n_w (m_w - m)^2], all terms positive), so no
 // digits are lost to a mean far from zero.
 //
-// The kernels read rows in aligned 16-byte accesses wherever a row starts:
+// The kernels read rows in aligned accesses wherever a row starts:
 // accesses are counted from the 16-byte boundary at or before the row's start, and
 // elements outside the row are left out.  A thread's rows lie a fixed stride apart
 // that keeps them at the same distance from such a boundary, so its columns,
@@ -137,11 +137,14 @@ enum class Fit { ALL, WHOLE, EDGES };
 
 // A row in registers, K accesses of W elements per lane: read once, one exchange
 // between its warps.  The bound is HBM (read x, write y) as long as an element costs
-// few instructions: 65,521 f16 rows of 8192 took 476 us at 27 per element and take 366
-// at 18, two at a time and without a branch.  Rows with edges walk the matrix with a
+// few instructions: 65,521 f16 rows of 8192 took 476 us at 27 per element and take 366 at 18,
+// two elements at a time and without a branch (5.9 TB/s, 86% of the copy rate; 40,000
+// binary32 rows of 2048: 101 us, 95%).  Rows with edges walk the matrix with a
 // fixed grid and keep the parameters in shared memory in binary32, (weight, bias)
 // of column c at [c mod W][c / W]: wherever a row starts, a warp reads neighbours.
-// The others have a block of threads each and read the parameters from L1.
+// The others have a block of threads each and read the parameters from L1.  (Measured and
+// dropped: a fixed grid with the next row on its way to shared memory, 386 us; 48
+// registers for 1280 threads per SM, 457 us, it spills.)
 template <typename T, typename P, int W, int K, Fit FIT>
 __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_t stride,
                                                   int pitch) {
@@ -350,14 +353,17 @@ constexpr int GRAD_STAGES = sizeof(T) == 4 ? 3 : 4;
 
 // Elements outside the row (EDGES: any row whose threads' accesses are not all whole and in
 // it) are masked, not branched around: a branch per access kept the others waiting
-// (32,768 x 4096 bf16: 219 us with them, 142 without).
+// (32,768 x 4096 bf16 with branches: 219 us).
 //
 // dx, and this group's share of dweight and dbias, in one pass over dy and x: a row's
 // threads walk the rows with a fixed stride, the rows ahead on their way to shared
 // memory (each lane's accesses in slots of its own), and keep their columns' sums of
 // dy * xhat and dy in registers to the end.  GIVEN: rows of more than GRAD_COLUMNS
 // columns, in tiles of as many (blockIdx.y); the row's two means come from
-// grad_means and nothing is exchanged.  The bound is HBM (read dy and x, write dx).
+// grad_means and nothing is exchanged.  The bound is HBM (read dy and x, write dx):
+// 32,768 rows of 4096 bf16 142 us with the join, 5.7 TB/s (84% of the copy rate), 30,000
+// binary32 rows of 4096 240 us (91%).  128 registers hold the sums, which leaves 16 warps
+// per SM; 64 or 80 registers spill and take 220 us or more.
 // part: [slices, or blocks of narrow rows][2][dim].
 template <typename T, typename P, int W, int K, Fit FIT, bool GIVEN>
 __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p, Layout l,
@@ -375,7 +381,8 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
     const int slice = blockIdx.x * l.rows + in_block;
     int64_t r = slice, first = r - lane / l.lanes;
     // the tile's accesses follow the ones of the tiles before, so none is in two tiles
-    const int c0 = tid * W - (EDGES ? lead_of(x.row(r), W * (int)sizeof(T)) : 0) + (GIVEN ? (int)blockIdx.y * GRAD_COLUMNS : 0);
+    const int c0 = tid * W - (EDGES ? lead_of(x.row(r), W * (int)sizeof(T)) : 0) +
+                   (GIVEN ? (int)blockIdx.y * GRAD_COLUMNS : 0);
     const int step = threads * W;
     auto in = [&](int k) { return FIT == Fit::ALL || c0 + k * step < dim; };
     auto fetch = [&](int64_t row, int stage) {
@@ -599,7 +606,8 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
 }
 
 // The two means of each row: a block per row.  W == 1 where x and dy lie differently
-// against 16-byte boundaries.
+// against 16-byte boundaries.  Wide rows read dy and x twice so: 18,000 of 16,384 bf16
+// take 490 us, 5 passes over memory where 3 are needed (261 us).
 template <typename T, typename P, int W>
 __global__ __launch_bounds__(ANY_THREADS) void grad_means(NormGradParams p) {
     __shared__ float s[ANY_THREADS / 32];
@@ -672,7 +680,7 @@ __global__ __launch_bounds__(ANY_THREADS) void norm_grad_any(NormGradParams p) {
 // dweight and dbias from the slices' partial sums: a block takes 32 columns, each
 // of its warps every JOIN_WARPS-th slice in order, then the warps' sums are added
 // in order.  As many warps as a block may have: the sums are short, and what
-// counts is how many loads wait together.
+// counts is how many loads wait together (608 slices of 4096 columns: 6 us).
 constexpr int JOIN_WARPS = 32;
 template <typename P>
 __global__ __launch_bounds__(32 * JOIN_WARPS) void norm_dw_join(NormGradParams p, int slices) {

@@ -452,7 +452,9 @@ spmm_status_t spmm_csr_f32_noalloc(float alpha,
  * any base address that suits the element type, and any leading dimension,
  * is accepted (16-byte aligned rows are the fast case).  An output must not
  * overlap an input unless the call says so.  Results are deterministic: no
- * floating-point atomics, every sum in a fixed order.
+ * floating-point atomics, every sum in a fixed order for given sizes, strides and
+ * addresses modulo 16.  Columns (dim) are at most 2^30, rows, tokens, ids and
+ * vocab at most 2^31 - 2.
  *
  * The calls are asynchronous on `stream`; the current device must be the
  * handle's (SPMM_ERR_INVALID_ARGUMENT).  Scratch, where a call needs some, is
@@ -486,9 +488,9 @@ spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale,
  * type `type`, dtable `grad_type`, which is `type` or SPMM_F32.  The tokens are
  * sorted by id on the device (stable), and each row's sum is taken in binary32
  * over pieces of consecutive sorted tokens whose bounds depend on `tokens`
- * and `dim` alone, then over the pieces in order.  Scratch: 16 bytes per token,
- * and for the rows that pieces share 8 bytes per element of dout or, where that
- * is less, about 34 MB or 1/32 byte per element, the larger.  tokens <= 2^30. */
+ * and `dim` alone, then over the pieces in order.  Scratch: two 8-byte keys per
+ * token, and at most 8 bytes per element of dout (for long inputs about 18 MB
+ * or 1/32 byte per element, the larger).  tokens <= 2^30. */
 spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t grad_type,
                                   float scale, const int32_t *ids, int64_t tokens,
                                   const void *dout, int64_t ld_dout, float beta,
@@ -516,8 +518,9 @@ spmm_status_t spmm_layer_norm(spmm_handle_t h, spmm_type_t type, spmm_type_t par
  * dx has type `type` and may be dy; dweight and dbias have type `param_type`
  * (either may be NULL: not computed) and are overwritten (zeros for
  * rows == 0).  weight NULL means 1.  mean and rstd as spmm_layer_norm wrote
- * them.  Scratch: 8 bytes per column for each slice of the rows, of which there
- * are at most 32 per SM or rows / 256, the larger, and no more than rows. */
+ * them.  Scratch: 8 bytes per row, and 8 bytes per column for each slice of the
+ * rows, of which there are at most 16 per SM or rows / 256, the larger, and no
+ * more than rows. */
 spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t param_type,
                                    const void *dy, int64_t ld_dy, const void *x, int64_t ldx,
                                    const float *mean, const float *rstd, const void *weight,
@@ -537,8 +540,9 @@ spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_
  * and log probability -inf.  A row without an unmasked logit (vocab == 0 too)
  * has lse = -inf, entropy 0 and logprob -inf (0 without a target).  A NaN or
  * +inf among the logits makes the row's lse, entropy, logprob and top_logprob
- * NaN; NaNs are never alternatives.  The order of the alternatives is that of
- * the logits themselves, before alpha.
+ * NaN; NaNs are never alternatives.  z is formed in binary32, so a finite logit
+ * that alpha takes beyond its range counts as an infinite one.  The order of the
+ * alternatives is that of the logits themselves, before alpha.
  * All outputs but top_index are binary32.  targets and logprob may be NULL
  * together, entropy and lse each, top_logprob and top_index when top_k == 0.
  * 0 <= top_k <= 32.  One pass over the logits, one launch, no scratch. */
