@@ -15,7 +15,7 @@ namespace {
 
 constexpr int64_t MAX_COUNT = INT_MAX - 1;      // rows, tokens, ids: 32-bit indices
 constexpr int64_t MAX_TOKENS = 1LL << 30;       // sorted tokens: room for padding in 32 bits
-constexpr int64_t MAX_WIDTH = 1LL << 30;        // columns, likewise
+constexpr int64_t MAX_WIDTH = 1LL << 28;        // columns, likewise, and as grid rows of 8192
 
 inline bool bad_type(spmm_type_t t) { return t != SPMM_F32 && t != SPMM_F16 && t != SPMM_BF16; }
 // Parameters and gradients have the operands' type or binary32.

@@ -203,18 +203,14 @@ __device__ __forceinline__ int lead_of(const T* row, int bytes) {
     return (int)(reinterpret_cast<uintptr_t>(row) % bytes / sizeof(T));
 }
 
-// Asynchronous copies of a Vec into the issuing thread's own slot of shared
+// Asynchronous copies of a 16-byte Vec into the issuing thread's own slot of shared
 // memory: no registers wait for them, and since no other thread reads the slot,
-// no barrier is needed either.  4 or 16 bytes (single 16-bit elements have none).
-template <typename T, int W>
-constexpr bool can_copy_async = sizeof(T) * W >= 4;
+// no barrier is needed either.
 template <typename T, int W>
 __device__ __forceinline__ void copy_async(Vec<T, W>* to, const T* from) {
+    static_assert(sizeof(T) * W == 16);
     const unsigned a = (unsigned)__cvta_generic_to_shared(to);
-    if constexpr (sizeof(T) * W == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(a), "l"(from) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_issued() {
     asm volatile("cp.async.commit_group;" ::: "memory");

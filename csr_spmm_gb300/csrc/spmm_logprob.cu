@@ -179,6 +179,7 @@ struct RowShared {
     unsigned short chosen[32 * LP_WARPS * UNITS];   // groups that hold the alternatives
     int chosen_count;
     int count;
+    unsigned bound[LP_WARPS];                   // a number that some of the warp's lanes reach
     uint64_t list[CANDIDATES];
 };
 
@@ -245,47 +246,73 @@ __device__ void collect(RowShared& sh, const Row<T>& row, const Part& part, int 
     }
 }
 
-// The alternatives of this block's part of the row, into sh.best.
-//
-// group[i] is the order of the largest logit of this thread's i-th group.  A number tau
-// that the largest logits of k threads reach is a lower bound of the k-th largest
-// logit, and every logit that reaches it belongs to a group whose largest does.  So a
-// second look (in L2) at those groups, little more than k of the block's 1024, gives
-// a short list that holds the alternatives; its entries are ranked by counting.
-// When more than CANDIDATES logits reach tau, it is raised to the k-th largest of the
-// threads' largest, which nearly all of them must equal then: the list is made of those
-// above tau, and the first equal ones in index order.
-template <typename T>
-__device__ void choose(RowShared& sh, const Row<T>& row, const Part& part,
-                       const unsigned (&group)[UNITS], int k) {
-    constexpr int W = Row<T>::W;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    unsigned mine = 0;
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i) mine = max(mine, group[i]);
-    // tau: bit by bit below what all threads' values have in common, until exactly k
-    // reach it (0: fewer than k have any)
-    const unsigned wmax = __reduce_max_sync(ALL, mine), wmin = __reduce_min_sync(ALL, mine);
-    if (lane == 0) sh.list[w] = (uint64_t)wmax << 32 | wmin;
-    __syncthreads();
-    unsigned most = wmax, fewest = wmin;
-    for (int i = 0; i < part.warps; ++i) {
-        most = max(most, (unsigned)(sh.list[i] >> 32));
-        fewest = min(fewest, (unsigned)sh.list[i]);
+// The `many`-th largest of the lanes' values (0: that many have none).
+__device__ __forceinline__ unsigned warp_nth(unsigned x, int many, int lane) {
+    unsigned m = 0;
+    for (int i = 0; i < many; ++i) {
+        m = __reduce_max_sync(ALL, x);
+        if (lane == __ffs(__ballot_sync(ALL, x == m)) - 1) x = 0;
     }
-    int bit = most == fewest ? -1 : 31 - __clz(most ^ fewest);
-    unsigned tau = bit < 0 ? most : bit == 31 ? 0 : most >> (bit + 1) << (bit + 1);
+    return m;
+}
+
+// A number that at least k threads' values reach (0: fewer have any), bit by bit from
+// what is known of it, `bit` the next to look at.  ENOUGH: until exactly k reach it, else
+// to the end: the k-th largest itself.
+template <bool ENOUGH>
+__device__ __forceinline__ unsigned block_nth(unsigned x, int k, unsigned tau, int bit) {
     int reach = 0;
-    for (; bit >= 0 && reach != k; --bit) {
+    for (; bit >= 0 && !(ENOUGH && reach == k); --bit) {
         const unsigned next = tau | 1u << bit;
-        const int n = __syncthreads_count(mine >= next);
+        const int n = __syncthreads_count(x >= next);
         if (n < k) continue;
         tau = next;
         reach = n;
     }
-    if (tid < k) sh.best[tid] = 0;
-    if (tid == 0) sh.chosen_count = sh.count = 0;
-    __syncthreads();
+    return tau;
+}
+
+// The alternatives of this block's part of the row, into sh.best.
+//
+// group[i] is the order of the largest logit of this thread's i-th group, `mine` the
+// largest of them.  A number tau that the largest logits of k threads reach is a lower
+// bound of the k-th largest logit, and every logit that reaches it belongs to a group
+// whose largest does.  So a second look (in L2) at those groups, few of the block's
+// 1024, gives a short list that holds the alternatives; its entries are ranked by
+// counting.  tau is searched until exactly k threads reach it.  QUICK: it is the least
+// of the warps' n-th largest, n their share of k (sh.bound, before the call's barrier):
+// fewer barriers for some more groups, which pays where a call is short (8 rows of 131,072
+// bf16: 7.7 us, 8.6 without) and costs where it is not (4099 rows of 50,001: 154, 146
+// without).
+// When more than CANDIDATES logits reach tau, it is raised to the k-th largest of the
+// threads' largest, which nearly all of them must equal then: the list is made of those
+// above tau, and the first equal ones in index order.
+template <typename T, bool QUICK>
+__device__ void choose(RowShared& sh, const Row<T>& row, const Part& part,
+                       const unsigned (&group)[UNITS], unsigned mine, int k) {
+    constexpr int W = Row<T>::W;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    unsigned tau;
+    if constexpr (QUICK) {
+        tau = sh.bound[0];
+        for (int i = 1; i < part.warps; ++i) tau = min(tau, sh.bound[i]);
+        // a warp without enough logits (past the row's end, masked) says nothing of the others
+        if (tau == 0) tau = block_nth<true>(mine, k, 0, 31);
+    } else {
+        // from the bits that all threads' values have in common
+        const unsigned wmax = __reduce_max_sync(ALL, mine), wmin = __reduce_min_sync(ALL, mine);
+        if (lane == 0) sh.list[w] = (uint64_t)wmax << 32 | wmin;
+        __syncthreads();
+        unsigned most = wmax, fewest = wmin;
+        for (int i = 0; i < part.warps; ++i) {
+            most = max(most, (unsigned)(sh.list[i] >> 32));
+            fewest = min(fewest, (unsigned)sh.list[i]);
+        }
+        const int bit = most == fewest ? -1 : 31 - __clz(most ^ fewest);
+        tau = bit < 0 ? most : bit == 31 ? 0 : most >> (bit + 1) << (bit + 1);
+        tau = block_nth<true>(mine, k, tau, bit);
+        __syncthreads();                            // the list is free again
+    }
     const unsigned least = max(tau, 1u);
 #pragma unroll
     for (int i = 0; i < UNITS; ++i)
@@ -296,11 +323,7 @@ __device__ void choose(RowShared& sh, const Row<T>& row, const Part& part,
     collect(sh, row, part, chosen, least);
     __syncthreads();
     if (sh.count > CANDIDATES) {
-        // the k-th largest itself: the bits that were left out
-        for (; bit >= 0; --bit) {
-            const unsigned next = tau | 1u << bit;
-            if (__syncthreads_count(mine >= next) >= k) tau = next;
-        }
+        tau = block_nth<false>(mine, k, 0, 31);
         __syncthreads();
         if (tid == 0) sh.count = 0;
         __syncthreads();
@@ -376,10 +399,10 @@ __device__ void choose(RowShared& sh, const Row<T>& row, const Part& part,
     for (int a = tid; a < n; a += blockDim.x) {
         const uint64_t key = sh.list[a];
         int place = 0;
+#pragma unroll 4
         for (int b = 0; b < n; ++b) place += sh.list[b] > key;
         if (place < k) sh.best[place] = key;
     }
-    __syncthreads();
 }
 
 // A block (SPLIT: one of a cluster's blocks, each with an equal share of the
@@ -483,17 +506,26 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
     }
     a = join(a, c, low);
     if (lane == 0) sh.sums[w] = a;
+    unsigned group[UNITS], mine = 0;
+    if constexpr (TOP) {
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            group[i] = order_of(top[i].value());
+            mine = max(mine, group[i]);
+        }
+        if constexpr (SPLIT) {
+            const unsigned bound = warp_nth(mine, (p.top_k + warps - 1) / warps, lane);
+            if (lane == 0) sh.bound[w] = bound;
+        }
+        if (tid < p.top_k) sh.best[tid] = 0;
+        if (tid == 0) sh.chosen_count = sh.count = 0;
+    }
     __syncthreads();
     if (w == 0) {
         a = join(lane < warps ? sh.sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, c, low);
         if (lane == 0) sh.total = a;
     }
-    if constexpr (TOP) {
-        unsigned group[UNITS];
-#pragma unroll
-        for (int i = 0; i < UNITS; ++i) group[i] = order_of(top[i].value());
-        choose(sh, row, part, group, p.top_k);
-    }
+    if constexpr (TOP) choose<T, SPLIT>(sh, row, part, group, mine, p.top_k);
     __syncthreads();
     a = sh.total;
     if constexpr (SPLIT) {

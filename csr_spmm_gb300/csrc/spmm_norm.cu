@@ -651,15 +651,17 @@ __global__ __launch_bounds__(ANY_THREADS) void grad_means(NormGradParams p) {
 
 // Where x, dy and dx lie differently against 16-byte boundaries: element by element,
 // a thread per column and slice of the rows, the row's means from grad_means.
-constexpr int SLICE_ROWS = 256;
+constexpr int64_t SLICE_ROWS = 256, SLICES = 32768;      // rows at least, slices at most
+int64_t slice_rows(int64_t rows) { return std::max(SLICE_ROWS, (rows + SLICES - 1) / SLICES); }
+int64_t slices_any(int64_t rows) { return (rows + slice_rows(rows) - 1) / slice_rows(rows); }
 template <typename T, typename P>
-__global__ __launch_bounds__(ANY_THREADS) void norm_grad_any(NormGradParams p) {
+__global__ __launch_bounds__(ANY_THREADS) void norm_grad_any(NormGradParams p, int64_t slice) {
     const int64_t c = (int64_t)blockIdx.x * ANY_THREADS + threadIdx.x;
     if (c >= p.dim) return;
     const float w = param<P>(p.weight, c, 1.0f);
     float dw = 0.0f, db = 0.0f;
-    const int64_t r0 = (int64_t)blockIdx.y * SLICE_ROWS;
-    const int64_t r1 = min(r0 + SLICE_ROWS, p.rows);
+    const int64_t r0 = (int64_t)blockIdx.y * slice;
+    const int64_t r1 = min(r0 + slice, p.rows);
 #pragma unroll 4
     for (int64_t r = r0; r < r1; ++r) {
         const float g = to_f32(static_cast<const T*>(p.dy)[r * p.ld_dy + c]);
@@ -767,7 +769,6 @@ cudaError_t norm_launch(const NormParams& p, int64_t columns, int num_sms, cudaS
 int64_t slices_most(int num_sms, const Layout& l) {
     return (int64_t)num_sms * l.rows * std::max(1, GRAD_THREADS / (l.threads() * l.rows));
 }
-int64_t slices_any(int64_t rows) { return (rows + SLICE_ROWS - 1) / SLICE_ROWS; }
 
 template <typename T, typename P, bool GIVEN>
 cudaError_t norm_grad_launch(const NormGradParams& p, int64_t columns, int num_sms,
@@ -836,8 +837,9 @@ cudaError_t launch_layer_norm(spmm_type_t type, spmm_type_t param_type, const No
 
 size_t norm_grad_scratch(int64_t rows, int64_t dim, int num_sms) {
     // a row group per warp at most; and the rows' means
-    const int64_t slices = std::max(
-        slices_any(rows), std::min<int64_t>(rows, (int64_t)num_sms * (GRAD_THREADS / 32)));
+    const int64_t slices =
+        std::max(std::min((rows + SLICE_ROWS - 1) / SLICE_ROWS, SLICES),
+                 std::min<int64_t>(rows, (int64_t)num_sms * (GRAD_THREADS / 32)));
     return ((size_t)slices * 2 * (size_t)dim + (size_t)rows * 2) * sizeof(float);
 }
 
@@ -873,7 +875,7 @@ cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,
                     slices = (int)slices_any(p.rows);
                     const dim3 grid((unsigned)((p.dim + ANY_THREADS - 1) / ANY_THREADS),
                                     (unsigned)slices);
-                    norm_grad_any<T, P><<<grid, ANY_THREADS, 0, st>>>(p);
+                    norm_grad_any<T, P><<<grid, ANY_THREADS, 0, st>>>(p, slice_rows(p.rows));
                     e = cudaGetLastError();
                 }
             }

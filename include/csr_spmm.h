@@ -453,7 +453,7 @@ spmm_status_t spmm_csr_f32_noalloc(float alpha,
  * is accepted (16-byte aligned rows are the fast case).  An output must not
  * overlap an input unless the call says so.  Results are deterministic: no
  * floating-point atomics, every sum in a fixed order for given sizes, strides and
- * addresses modulo 16.  Columns (dim) are at most 2^30, rows, tokens, ids and
+ * addresses modulo 16.  Columns (dim) are at most 2^28, rows, tokens, ids and
  * vocab at most 2^31 - 2.
  *
  * The calls are asynchronous on `stream`; the current device must be the
