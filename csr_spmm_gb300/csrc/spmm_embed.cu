@@ -247,8 +247,9 @@ __global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restri
 // the last of those sums to arrive adds them in order: a token that makes up a
 // tenth of 300,000 has near a thousand pieces.  Warps behind those of the sums write the
 // rows without a token.  The bound is HBM: 65,536 tokens of 4096 bf16 into a table of
-// 131,072 binary32 rows take 414 us with the sort, 6.5 TB/s of what must move (95% of
-// the copy rate).
+// 131,072 binary32 rows take 409 us with the sort, 6.5 TB/s of what must move (96% of
+// the copy rate).  80 registers for three blocks per SM (some spill in the joins): 414 us
+// with 99 and two, and where rows are added to instead of written 294 us against 252.
 constexpr int PANEL = 256;           // columns per warp: 512 bytes of a 16-bit row
 constexpr int PIECE_MAX = 256;
 constexpr int64_t SUM_WARPS = 8192;
@@ -399,7 +400,7 @@ struct GradSum {
     // Adds the partials of every `stride`-th piece from `from` to `to`; of the run's first
     // piece `first` it is the second one.
     __device__ void add_partials(int64_t from, int64_t to, int64_t stride, int64_t first) {
-        constexpr int MANY = 8;
+        constexpr int MANY = 32 / (V * W);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -599,7 +600,7 @@ __device__ void fill_rows(const EmbedGradParams& p, const GradWork& k, int64_t i
 }
 
 template <typename T, typename G, bool EDGES>
-__global__ __launch_bounds__(256) void grad_sums(EmbedGradParams p, GradWork k) {
+__global__ __launch_bounds__(256, 3) void grad_sums(EmbedGradParams p, GradWork k) {
     constexpr int W = 16 / (int)sizeof(T), V = PANEL / 32 / W;
     constexpr int BATCH = EDGES ? 4 / V : 8 / V;     // 8 words in flight per lane
     wait_for_predecessor();

@@ -411,9 +411,9 @@ __device__ void choose(RowShared& sh, const Row<T>& row, const Part& part,
 // same maxima serve the choice of the alternatives.  The bound is HBM (the row
 // once) while an element costs under about 9 instructions: 16-bit maxima and the floor
 // are taken two at a time before unpacking, products and sums two at a time after.
-// 8192 rows of 131,072 bf16: 307 us without alternatives (the copy rate), 367 us with 20
-// (86%): between a row's last access and the next row's first the block ranks, and the
-// SM's other blocks are not enough to fill that time.  8 rows with 8: 8.6 us in clusters
+// 8192 rows of 131,072 bf16: 308 us without alternatives (the copy rate), 372 us with 20
+// (85%): between a row's last access and the next row's first the block ranks, and the
+// SM's other blocks are not enough to fill that time.  8 rows with 8: 7.7 us in clusters
 // of 8 blocks.
 template <typename T, bool TOP, bool SPLIT>
 __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p, int split) {
@@ -615,7 +615,9 @@ cudaError_t launch_forward(const LogprobParams& p, int num_sms, cudaStream_t st)
     // 50 us with 2 warps, 39 with 1.
     int warps = LP_WARPS;
     const int64_t least = p.rows >= 4 * num_sms ? 8 * UNITS : 2 * UNITS;
-    while (warps > 1 && share < least * warps && split == 1) warps /= 2;
+    // the choice wants twice as many lanes as alternatives, and all it can get for few rows
+    const int most = p.rows >= 4 * num_sms ? (2 * p.top_k + 31) / 32 : p.top_k > 0 ? LP_WARPS : 1;
+    while (warps > most && warps > 1 && share < least * warps && split == 1) warps /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.rows * split));
     cfg.blockDim = dim3(32 * warps);
