@@ -32,8 +32,6 @@ from ._lib import (EXPORTED, SPMM_ERR_ALLOC, SPMM_ERR_CUDA, SPMM_ERR_DIMENSION_M
                    SPMM_F32, SPMM_F16, SPMM_BF16, SPMM_TOP_MAX, spmm_reserve_lm, spmm_embedding,
                    spmm_embedding_grad, spmm_layer_norm, spmm_layer_norm_grad, spmm_token_logprob,
                    spmm_token_logprob_grad)
-from .lm import (embedding, embedding_grad, layer_norm, layer_norm_grad, token_logprob,
-                 token_logprob_grad)
 
 __all__ = ["Handle", "spmm", "csr_check", "SpmmError", "library", "spmm_create", "spmm_destroy",
            "spmm_reserve", "spmm_csr_f32", "spmm_csr_f64", "spmm_csr_check", "status_string",
@@ -48,6 +46,21 @@ __all__ = ["Handle", "spmm", "csr_check", "SpmmError", "library", "spmm_create",
            "spmm_embedding_grad", "spmm_layer_norm", "spmm_layer_norm_grad",
            "spmm_token_logprob", "spmm_token_logprob_grad", "embedding", "embedding_grad",
            "layer_norm", "layer_norm_grad", "token_logprob", "token_logprob_grad", "EXPORTED"]
+
+
+_LM = ("embedding", "embedding_grad", "layer_norm", "layer_norm_grad", "token_logprob",
+       "token_logprob_grad")
+
+
+def __getattr__(name):
+    """The language-model operators, on first use: their module needs torch, which the C
+    entry points do without."""
+    if name in _LM or name == "lm":
+        import importlib
+        lm = importlib.import_module(".lm", __name__)
+        globals().update({n: getattr(lm, n) for n in _LM}, lm=lm)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class Handle:

@@ -145,3 +145,18 @@ def test_calls_pass_addresses_and_leading_dimensions(monkeypatch):
     with pytest.raises(ValueError, match="handle is on cuda:1"):
         cs.embedding(types.SimpleNamespace(ptr=1, device=1), ids, table, out=out)
     assert calls == []
+
+
+def test_the_package_imports_without_torch():
+    """torch is needed by the tensor wrappers only, and loaded on their first use."""
+    import subprocess
+    import sys
+    code = ("import sys; import csr_spmm_gb300 as cs; assert 'torch' not in sys.modules; "
+            "cs.SPMM_BF16; from csr_spmm_gb300 import embedding; assert 'torch' in sys.modules; "
+            "assert cs.embedding is embedding is cs.lm.embedding; "
+            "missing = False\ntry:\n    cs.nothing\nexcept AttributeError:\n    missing = True\n"
+            "assert missing")
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
