@@ -37,6 +37,21 @@ __device__ __forceinline__ float lanes_sum(float x, int lanes) {
     for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
     return x;
 }
+// Two of them at once: the exchanges of one wait beside the other's.
+__device__ __forceinline__ void lanes_sum(float& x, float& y, int lanes) {
+    if (lanes == 32) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(ALL, x, o);
+            y += __shfl_xor_sync(ALL, y, o);
+        }
+    } else {
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(ALL, x, o);
+            y += __shfl_xor_sync(ALL, y, o);
+        }
+    }
+}
 // Barrier of one row's warps (barrier 0 is the block's own).
 __device__ __forceinline__ void row_barrier(int row, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "r"(threads) : "memory");
@@ -512,9 +527,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
         } else {
             float lo, hi;
             halves(a2, lo, hi);
-            a = lanes_sum(lo + hi, l.lanes);
+            a = lo + hi;
             halves(b2, lo, hi);
-            b = lanes_sum(lo + hi, l.lanes);
+            b = lo + hi;
+            lanes_sum(a, b, FIT == Fit::ALL ? 32 : l.lanes);
             if (l.warps > 1) {
                 // two sets of slots in turn: one barrier per row keeps them apart
                 float2* s = slots[turn] + in_block * l.warps;
