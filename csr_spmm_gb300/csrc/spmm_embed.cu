@@ -251,15 +251,18 @@ __global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restri
 // the copy rate).  80 registers for three blocks per SM (some spill in the joins): 414 us
 // with 99 and two, and where rows are added to instead of written 294 us against 252.
 constexpr int PANEL = 256;           // columns per warp: 512 bytes of a 16-bit row
-constexpr int PIECE_MAX = 256;
-constexpr int64_t SUM_WARPS = 8192;
+constexpr int PIECE_MAX = 128;
+constexpr int64_t SUM_WARPS = 4096;
 constexpr int JOIN = 32;             // pieces of a run joined at once
 constexpr int COUNTERS = 3;          // per piece and panel
 
-// Tokens per piece: as many as leave about SUM_WARPS warps of work (three to four
-// times what the SMs hold at once), so that few runs are cut; one where there is
-// less, because a warp's tokens wait for one another.  It depends on the call's
-// sizes only, so the order of every sum does too.
+// Tokens per piece: as many as leave about SUM_WARPS warps of work (about what the SMs
+// hold at once), so that few runs are cut; one where there is less, because a warp's
+// tokens wait for one another.  8192 tokens of 2048 bf16 take 41 us with 4096 warps, 45
+// with 8192 and 43 with 2048; 1224 tokens of 6263 f16 added to their rows 34, 39 and 28,
+// but 20,000 of 2001 bf16 73, 74 and 97.  No piece is longer than PIECE_MAX: 65,536
+// tokens of 4096 bf16 added to binary32 rows take 251 us with 128 and 272 with 256.  It
+// depends on the call's sizes only, so the order of every sum does too.
 inline int64_t panels_of(int64_t dim) { return (dim + PANEL - 1) / PANEL; }
 inline int piece_of(int64_t tokens, int64_t dim) {
     int piece = 1;

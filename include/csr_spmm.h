@@ -489,8 +489,8 @@ spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale,
  * sorted by id on the device (stable), and each row's sum is taken in binary32
  * over pieces of consecutive sorted tokens whose bounds depend on `tokens`
  * and `dim` alone, then over the pieces in order.  Scratch: two 8-byte keys per
- * token, and at most 8 bytes per element of dout (for long inputs about 18 MB
- * or 1/32 byte per element, the larger).  tokens <= 2^30. */
+ * token, and at most 8 bytes per element of dout (for long inputs about 9 MB
+ * or 1/16 byte per element, the larger).  tokens <= 2^30. */
 spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t grad_type,
                                   float scale, const int32_t *ids, int64_t tokens,
                                   const void *dout, int64_t ld_dout, float beta,
