@@ -6,6 +6,7 @@
 // keys (id << 32 | position) are unique, so any correct sort of them is the
 // stable order, and the sums below have a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "spmm_internal.h"
 #include "spmm_lm_device.cuh"
@@ -19,15 +20,29 @@ namespace {
 constexpr int EMBED_THREADS = 256;
 constexpr int EMBED_BATCH = 4;       // accesses in flight per thread
 
+// The elements of an access times scale; padding: zeros, by its bits rather than element
+// by element.
+template <typename T, int W>
+__device__ __forceinline__ void scaled(Vec<T, W> got, int id, const EmbedParams& p, float (&f)[W]) {
+    const bool valid = id >= 0 && id < p.vocab;
+    const uint32_t keep = valid ? ~0u : 0u;
+#pragma unroll
+    for (int i = 0; i < Vec<T, W>::WORDS; ++i) got.w[i] &= keep;
+    const float scale = valid ? p.scale : 0.0f;
+    const uint64_t scale2 = pair(scale, scale);
+    unpack(got, f);
+#pragma unroll
+    for (int i = 0; i < W; i += 2) halves(mul2(pair(f[i], f[i + 1]), scale2), f[i], f[i + 1]);
+}
+
 // A block takes `block_rows` rows; its threads walk the rows' accesses in
 // order (nv accesses of 16 bytes per row, then the next row), so narrow
 // rows share a warp and the stores of neighbouring threads are contiguous.
-// EDGES: any width and alignment: accesses are those of out's aligned words, and
-// the table is read from wherever their elements lie.  The bound is HBM: one table
-// row read and one written per token.  100,003 Zipf-distributed tokens of 4096 bf16:
-// 172 us, 6.1 TB/s of distinct rows read and rows written (90% of the copy rate; 241 us
-// before a batch's accesses were free of branches and kept packed).
-template <typename T, bool EDGES>
+// The bound is HBM: one table row read and one written per token.  100,003
+// Zipf-distributed tokens of 4096 bf16: 172 us, 6.1 TB/s of distinct rows read and rows
+// written (90% of the copy rate; 241 us before a batch's accesses were free of branches
+// and kept packed).
+template <typename T>
 __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int nv,
                                                             int block_rows) {
     constexpr int W = 16 / (int)sizeof(T);
@@ -36,8 +51,6 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int n
     const int* ids = p.ids + row0;
     T* out = static_cast<T*>(p.out) + row0 * p.ld_out;
     const int rows = (int)min((int64_t)block_rows, p.tokens - row0);
-    const int dim = (int)p.dim;
-    const int64_t elements = (p.vocab - 1) * p.ld_table + p.dim;
     const int step_r = EMBED_THREADS / nv, step_c = EMBED_THREADS % nv;
     int r = threadIdx.x / nv, c = threadIdx.x % nv;
     while (r < rows) {
@@ -46,7 +59,6 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int n
         // on their way together
         int id[EMBED_BATCH], row[EMBED_BATCH], col[EMBED_BATCH];
         Vec<T, W> v[EMBED_BATCH];
-        Unaligned<T> far[EDGES ? EMBED_BATCH : 1];
 #pragma unroll
         for (int u = 0; u < EMBED_BATCH; ++u) {
             row[u] = r;
@@ -60,75 +72,145 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_rows(EmbedParams p, int n
             }
         }
         if (p.vocab > 0) {
-            if constexpr (EDGES) {
-                bool clear = true;
-                int64_t at[EMBED_BATCH];
 #pragma unroll
-                for (int u = 0; u < EMBED_BATCH; ++u) {
-                    const bool valid = id[u] >= 0 && id[u] < p.vocab;
-                    col[u] -= lead_of(out + min(row[u], rows - 1) * p.ld_out, 16);
-                    at[u] = (valid ? id[u] : p.vocab / 2) * p.ld_table + min(col[u], dim - 1);
-                    clear &= clear_of_ends<W>(at[u], elements);
-                }
-                if (clear) {
-#pragma unroll
-                    for (int u = 0; u < EMBED_BATCH; ++u) far[u].load(table + at[u]);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < EMBED_BATCH; ++u) {
-                        const bool valid = id[u] >= 0 && id[u] < p.vocab;
-                        far[u].a = load_some<T, W>(table + (valid ? id[u] : 0) * p.ld_table,
-                                                   col[u], dim);
-                        far[u].b = far[u].a;
-                        far[u].shift = 0;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < EMBED_BATCH; ++u) {
-                    const bool valid = id[u] >= 0 && id[u] < p.vocab;
-                    v[u] = load_vec<Cache::KEEP, T, W>(table + (valid ? id[u] : 0) * p.ld_table +
-                                                       col[u]);
-                }
+            for (int u = 0; u < EMBED_BATCH; ++u) {
+                const bool valid = id[u] >= 0 && id[u] < p.vocab;
+                v[u] = load_vec<Cache::KEEP, T, W>(table + (valid ? id[u] : 0) * p.ld_table +
+                                                   col[u]);
             }
         }
 #pragma unroll
         for (int u = 0; u < EMBED_BATCH; ++u) {
             if (row[u] >= rows) continue;
-            const bool valid = id[u] >= 0 && id[u] < p.vocab;
-            Vec<T, W> got = v[u];
-            if constexpr (EDGES) got = far[u].get();
-            // padding: zero bits, four at a time rather than element by element
-            const uint32_t keep = valid ? ~0u : 0u;
-#pragma unroll
-            for (int i = 0; i < Vec<T, W>::WORDS; ++i) got.w[i] &= keep;
-            const float scale = valid ? p.scale : 0.0f;
-            const uint64_t scale2 = pair(scale, scale);
             float f[W];
-            unpack(got, f);
+            scaled(v[u], id[u], p, f);
+            store_vec<Cache::STREAM, T, W>(out + row[u] * p.ld_out + col[u], f);
+        }
+    }
+}
+
+// Any width and alignment: accesses are those of out's aligned words, and the table is
+// read from wherever their elements lie, as the two aligned words around them.  What
+// places a row (its id, its first word, the shift between the two) is found once and
+// serves COLS accesses of each of its lanes (a power of two of them, a warp's where it has as
+// many accesses), or one where a thread takes ROWS rows: EMBED_BATCH in flight either way.
+// Where lanes of a warp have one row its shift is theirs, and the words it takes are chosen by
+// a branch.  A warp goes through its row part by part, because the parts share sectors, which
+// have to be written together; only few rows are spread over blockIdx.y.  100,000 x 2001
+// bf16 take 92 us (79% of the copy rate), 115 with the parts over the grid, 111 with four
+// rows per warp and 140 with accesses that place themselves one by one as above.
+template <typename T, int ROWS>
+__global__ __launch_bounds__(EMBED_THREADS, 4) void embed_shifted(EmbedParams p, int lanes_log,
+                                                                  int parts, int used) {
+    constexpr int W = 16 / (int)sizeof(T), COLS = EMBED_BATCH / ROWS;
+    const T* table = static_cast<const T*>(p.table);
+    const int lane = threadIdx.x & ((1 << lanes_log) - 1);
+    const int64_t row0 =
+        (((int64_t)blockIdx.x * EMBED_THREADS + threadIdx.x) >> lanes_log) * ROWS;
+    if (row0 >= p.tokens) return;
+    const int dim = (int)p.dim;
+    const int64_t elements = (p.vocab - 1) * p.ld_table + p.dim;
+    int id[ROWS], lead[ROWS], nv[ROWS];
+    int64_t at[ROWS];
+    T* to[ROWS];
+    bool clear = true;
 #pragma unroll
-            for (int i = 0; i < W; i += 2) halves(mul2(pair(f[i], f[i + 1]), scale2), f[i], f[i + 1]);
-            if (EDGES) store_some<T, W>(out + row[u] * p.ld_out, col[u], dim, f);
-            else store_vec<Cache::STREAM, T, W>(out + row[u] * p.ld_out + col[u], f);
+    for (int r = 0; r < ROWS; ++r) id[r] = p.ids[min(row0 + r, p.tokens - 1)];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        to[r] = static_cast<T*>(p.out) + min(row0 + r, p.tokens - 1) * p.ld_out;
+        lead[r] = lead_of(to[r], 16);
+        nv[r] = (dim + lead[r] + W - 1) / W;
+        const bool valid = id[r] >= 0 && id[r] < p.vocab;
+        // padding: some row away from the table's ends is read in vain
+        at[r] = (valid ? id[r] : p.vocab / 2) * p.ld_table;
+        // an access begins at most W - 1 elements before the row and at most at its last,
+        // and its aligned words reach from less than W before it to less than 2 W behind
+        clear &= at[r] >= 2 * W && at[r] + dim + 2 * W <= elements;
+    }
+    for (int part = blockIdx.y; part < parts; part += gridDim.y) {
+        const int first = part * used * 32 + lane;              // its accesses: 32 apart
+        Vec<T, W> v[ROWS][COLS];
+        if (clear) {
+            // all at once; past the row its last one again
+            Unaligned<T> far[ROWS][COLS];
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int u = 0; u < COLS; ++u)
+                    far[r][u].load(
+                        table + at[r] +
+                        (min(first + (u < used ? u * 32 : 0), nv[r] - 1) * W - lead[r]));
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                if constexpr (ROWS <= 2) {
+                    auto take = [&](auto word) {
+#pragma unroll
+                        for (int u = 0; u < COLS; ++u)
+                            v[r][u] = far[r][u].template from_word<decltype(word)::value>();
+                    };
+                    switch (far[r][0].shift / 4) {
+                        case 0: take(std::integral_constant<int, 0>{}); break;
+                        case 1: take(std::integral_constant<int, 1>{}); break;
+                        case 2: take(std::integral_constant<int, 2>{}); break;
+                        default: take(std::integral_constant<int, 3>{});
+                    }
+                } else {
+                    v[r][0] = far[r][0].get();
+                }
+            }
+        } else if (p.vocab > 0) {
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int u = 0; u < COLS; ++u)
+                    v[r][u] = load_some<T, W>(table + at[r], (first + u * 32) * W - lead[r], dim);
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (row0 + r >= p.tokens) break;
+#pragma unroll
+            for (int u = 0; u < COLS; ++u) {
+                if (u >= used) break;
+                float f[W];
+                scaled(v[r][u], id[r], p, f);
+                store_some<T, W>(to[r], (first + u * 32) * W - lead[r], dim, f);
+            }
         }
     }
 }
 
 template <typename T>
-cudaError_t launch_embed(const EmbedParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_embed(const EmbedParams& p, bool whole, int num_sms, cudaStream_t st) {
     constexpr int W = 16 / (int)sizeof(T);
-    const bool whole = p.dim % W == 0 && rows_aligned16(p.out, p.ld_out, sizeof(T)) &&
-                       (p.vocab == 0 || rows_aligned16(p.table, p.ld_table, sizeof(T)));
+    if (whole) {
+        // about 8 accesses per thread and block; fewer rows per block while that
+        // would leave SMs without a block
+        const int nv = (int)(p.dim / W);
+        int64_t rows = std::max<int64_t>(1, EMBED_THREADS * 8 / nv);
+        rows = std::max<int64_t>(1, std::min<int64_t>(rows, p.tokens / (4 * num_sms)));
+        const unsigned blocks = (unsigned)((p.tokens + rows - 1) / rows);
+        embed_rows<T><<<blocks, EMBED_THREADS, 0, st>>>(p, nv, (int)rows);
+        return cudaGetLastError();
+    }
     // a row between boundaries covers up to W - 1 elements more
-    const int nv = (int)((p.dim + (whole ? 0 : 2 * (W - 1))) / W);
-    // about 8 accesses per thread and block; fewer rows per block while that
-    // would leave SMs without a block
-    int64_t rows = std::max<int64_t>(1, EMBED_THREADS * 8 / nv);
-    rows = std::max<int64_t>(1, std::min<int64_t>(rows, p.tokens / (4 * num_sms)));
-    const unsigned blocks = (unsigned)((p.tokens + rows - 1) / rows);
-    if (whole) embed_rows<T, false><<<blocks, EMBED_THREADS, 0, st>>>(p, nv, (int)rows);
-    else embed_rows<T, true><<<blocks, EMBED_THREADS, 0, st>>>(p, nv, (int)rows);
-    return cudaGetLastError();
+    const int64_t nv = (p.dim + 2 * (W - 1)) / W;
+    int lanes_log = 0;
+    while (lanes_log < 5 && (1 << lanes_log) < nv) ++lanes_log;
+    const int lane_accesses = (int)((nv + 31) / 32);
+    const int rows = lane_accesses == 1 ? 4 : lane_accesses == 2 ? 2 : 1;
+    const int parts = (lane_accesses + EMBED_BATCH / rows - 1) / (EMBED_BATCH / rows);
+    const int used = (lane_accesses + parts - 1) / parts;
+    const int64_t block_rows = (int64_t)(EMBED_THREADS >> lanes_log) * rows;
+    const int64_t blocks = (p.tokens + block_rows - 1) / block_rows;
+    const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(
+                                          parts, std::max<int64_t>(1, 4 * num_sms / blocks)));
+    auto run = [&](auto kernel) {
+        kernel<<<grid, EMBED_THREADS, 0, st>>>(p, lanes_log, parts, used);
+        return cudaGetLastError();
+    };
+    return rows == 4   ? run(embed_shifted<T, 4>)
+           : rows == 2 ? run(embed_shifted<T, 2>) : run(embed_shifted<T, 1>);
 }
 
 // ---- gradient: sort ------------------------------------------------------------
@@ -643,7 +725,11 @@ GradLayout grad_layout(int64_t tokens, int64_t dim) {
 
 cudaError_t launch_embedding(spmm_type_t type, const EmbedParams& p, int num_sms,
                              cudaStream_t st) {
-    return with_type(type, [&](auto t) { return launch_embed<decltype(t)>(p, num_sms, st); });
+    const bool whole = p.dim * lm_elem_size(type) % 16 == 0 &&
+                       rows_aligned16(p.out, p.ld_out, lm_elem_size(type)) &&
+                       (p.vocab == 0 || rows_aligned16(p.table, p.ld_table, lm_elem_size(type)));
+    return with_type(type,
+                     [&](auto t) { return launch_embed<decltype(t)>(p, whole, num_sms, st); });
 }
 
 size_t embed_grad_scratch(int64_t tokens, int64_t dim) { return grad_layout(tokens, dim).total; }

@@ -156,6 +156,16 @@ struct Unaligned {
         for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(u[i], u[i + 1], (shift & 2) * 8);
         return r;
     }
+    // The same where the shift is known to begin in word F of the first.
+    template <int F>
+    __device__ __forceinline__ Vec<T, W> from_word() const {
+        const uint32_t w[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
+        Vec<T, W> r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = __funnelshift_r(w[F + i], w[F + i + 1], (shift & 2) * 8);
+        return r;
+    }
 };
 // A matrix whose rows are read so: whether W elements from element `at` of the matrix
 // (rows and gaps) can be, i.e. no aligned word of theirs reaches over its ends.
@@ -186,16 +196,28 @@ __device__ __forceinline__ Vec<T, W> load_some(const T* row, int c, int dim) {
     return r;
 }
 // Stores W elements to [c, c + W) of a row of `dim`, a whole access at once (it must be
-// aligned then), those of another that lie in the row one by one.
+// aligned either way), those of another that lie in the row one by one or, of 16 bits, in pairs.
 template <typename T, int W>
 __device__ __forceinline__ void store_some(T* row, int c, int dim, const float (&f)[W]) {
     if (c >= 0 && c + W <= dim) {
         store_vec<Cache::STREAM, T, W>(row + c, f);
         return;
     }
+    if constexpr (sizeof(T) == 2 && W > 1) {
+        // words with both elements in the row at once
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-        if (c + i >= 0 && c + i < dim) row[c + i] = from_f32<T>(f[i]);
+        for (int i = 0; i < W; i += 2) {
+            const bool low = (unsigned)(c + i) < (unsigned)dim;
+            const bool high = (unsigned)(c + i + 1) < (unsigned)dim;
+            if (low & high) *reinterpret_cast<uint32_t*>(row + c + i) = pack_word(f + i, T{});
+            else if (low) row[c + i] = from_f32<T>(f[i]);
+            else if (high) row[c + i + 1] = from_f32<T>(f[i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if ((unsigned)(c + i) < (unsigned)dim) row[c + i] = from_f32<T>(f[i]);
+    }
 }
 // Columns before the row's start that its first aligned access of `bytes` covers.
 template <typename T>
