@@ -27,6 +27,9 @@ LIB = os.path.join(LIB_DIR, "libcsrspmm.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
+# The CUDA runtime is the process's shared one.  A second, static one costs 2.3 us (of 12)
+# in each small call between torch's own: a lookup that makes its output takes 9.6 us.
+LINK_FLAGS = ["-shared", "--cudart", "shared"]
 
 
 def _nvcc() -> str:
@@ -34,6 +37,12 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build csr_spmm_gb300")
+
+
+def _runtime_path(nvcc: str) -> list:
+    """Where the library finds libcudart when no one in the process has loaded it."""
+    lib = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "lib64")
+    return ["-Xlinker", "-rpath," + lib] if os.path.isdir(lib) else []
 
 
 def _sources():
@@ -49,7 +58,7 @@ def _digest(units, deps, extra) -> str:
             h.update(name.encode() + b"\0" + f.read())
     with open(os.path.join(INCLUDE, "csr_spmm.h"), "rb") as f:
         h.update(f.read())
-    h.update(" ".join(NVCC_FLAGS + list(extra)).encode())
+    h.update(" ".join(NVCC_FLAGS + LINK_FLAGS + list(extra)).encode())
     return h.hexdigest()
 
 
@@ -99,7 +108,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), out: str =
     with ThreadPoolExecutor(max_workers=max(1, min(len(units), os.cpu_count() or 4))) as ex:
         objs = list(ex.map(compile_one, units))
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc] + ARCH + ["-shared", "--cudart", "static", "-o", tmp] + objs
+    cmd = [nvcc] + ARCH + LINK_FLAGS + _runtime_path(nvcc) + ["-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
