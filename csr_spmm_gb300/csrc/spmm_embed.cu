@@ -6,6 +6,7 @@
 // keys (id << 32 | position) are unique, so any correct sort of them is the
 // stable order, and the sums below have a fixed order.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "spmm_internal.h"
@@ -217,6 +218,10 @@ cudaError_t launch_embed(const EmbedParams& p, bool whole, int num_sms, cudaStre
 
 constexpr int SORT_TILE = 512;       // keys sorted by one block, one per thread
 constexpr int MERGE_WAYS = 16;       // sorted runs merged per round, at most
+// From so many keys on the searches cost more than the launches they save, and fours
+// merged round by round have the fewest: 300,000 tokens of 64 columns take 135 us, with 16
+// runs to a round 167; 65,536 tokens the same either way.
+constexpr unsigned MERGE_MANY = 32768;
 constexpr unsigned NO_ID = 0xfffffffdu;  // of padding tokens
 constexpr unsigned REST = 0xfffffffeu;   // behind them, what fills the last tile
 
@@ -346,10 +351,13 @@ constexpr int COUNTERS = 3;          // per piece and panel
 // tokens of 4096 bf16 added to binary32 rows take 251 us with 128 and 272 with 256.  It
 // depends on the call's sizes only, so the order of every sum does too.
 inline int64_t panels_of(int64_t dim) { return (dim + PANEL - 1) / PANEL; }
-inline int piece_of(int64_t tokens, int64_t dim) {
-    int piece = 1;
-    while (piece < PIECE_MAX && tokens * panels_of(dim) / piece > SUM_WARPS) piece *= 2;
-    return piece;
+inline int piece_log_of(int64_t tokens, int64_t dim) {
+    int log = 0;
+    while ((1 << log) < PIECE_MAX && (tokens * panels_of(dim) >> log) > SUM_WARPS) ++log;
+    return log;
+}
+inline int64_t pieces_of(int64_t tokens, int piece_log) {
+    return (tokens + (1 << piece_log) - 1) >> piece_log;
 }
 // A partial row: whole accesses of 32 bytes, one more for rows between boundaries.
 inline int64_t padded(int64_t dim) { return (dim + 7) / 8 * 8 + 8; }
@@ -359,7 +367,8 @@ struct GradWork {
     float* partials;                 // [pieces][2][padded dim]: run from before, run to the next
     int* arrived;                    // [COUNTERS][pieces][panels], zeroed by sort_tiles
     int64_t dim_padded;
-    int piece;
+    int piece_log;                   // tokens per piece: a power of two
+    int pieces;
     int panels;
     int64_t sum_items;               // pieces * panels warps sum; the rest fill
     int fill_rows;                   // table rows per filling warp
@@ -465,37 +474,40 @@ struct GradSum {
     __device__ float* partial(int64_t slot) const { return k.partials + slot * k.dim_padded; }
     __device__ bool inside(int v) const { return column(v, lead) < dim; }
     // Keep the sum of a run that crosses the piece's bounds.
-    __device__ void leave_partial(int64_t piece, bool from_before) {
-        float* to = partial(2 * piece + (from_before ? 0 : 1));
+    __device__ void leave_partial(int piece, bool from_before) {
+        float* to = partial(2 * (int64_t)piece + (from_before ? 0 : 1));
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (inside(v)) store_vec<Cache::KEEP, float, W>(to + column(v, 0), acc[v]);
     }
     // Whether this warp is the last of `all` to come to a counter; what the others wrote
-    // before is visible then.
+    // before is visible then: one lane's count releases what its warp wrote and acquires
+    // what the warps counted before it did (a fence of every lane on both sides costs more).
     __device__ bool last_of(int64_t counter, int panel, int64_t all) const {
-        __threadfence();
+        unsigned before = 0;
         __syncwarp();
-        int before = 0;
-        if (lane == 0) before = atomicAdd(k.arrived + counter * k.panels + panel, 1);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        __threadfence();
-        return before == all - 1;
+        if (lane == 0)
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                         : "=r"(before)
+                         : "l"(k.arrived + counter * k.panels + panel)
+                         : "memory");
+        __syncwarp();
+        return __shfl_sync(0xffffffffu, before, 0) == all - 1;
     }
     // Adds the partials of every `stride`-th piece from `from` to `to`; of the run's first
     // piece `first` it is the second one.
-    __device__ void add_partials(int64_t from, int64_t to, int64_t stride, int64_t first) {
+    __device__ void add_partials(int from, int to, int stride, int first) {
         constexpr int MANY = 32 / (V * W);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[v][i] = 0.0f;
-        for (int64_t q = from; q <= to; q += MANY * stride) {
+        for (int q = from; q <= to; q += MANY * stride) {
             float got[MANY][V][W];
 #pragma unroll
             for (int u = 0; u < MANY; ++u) {
-                const int64_t piece = q + u * stride <= to ? q + u * stride : q;
-                const float* part = partial(2 * piece + (piece == first));
+                const int piece = q + u * stride <= to ? q + u * stride : q;
+                const float* part = partial(2 * (int64_t)piece + (piece == first));
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -511,28 +523,48 @@ struct GradSum {
                         acc[v][i] += q + u * stride <= to ? got[u][v][i] : 0.0f;
         }
     }
-    // This piece's part of the run of `id` is kept: the last to come here joins the parts.
-    __device__ void join(int64_t piece, unsigned id, int panel) {
+    // The first and the last piece of the run of `id`, which goes through `piece`'s bounds.
+    __device__ void run_pieces(int piece, unsigned id, int& first, int& last) const {
+        // The pieces' own first keys tell how far the run goes on, the keys before them
+        // whether it came from before: 32 of each at once.
+        const int behind = piece + 1 + lane, before = piece - lane;
+        const unsigned at = (unsigned)min(behind, k.pieces - 1) << k.piece_log;
+        const unsigned from = (unsigned)max(before, 1) << k.piece_log;
+        const bool goes_on = (unsigned)(k.keys[at] >> 32) == id && behind < k.pieces;
+        const bool came = (unsigned)(k.keys[min((int64_t)from, p.tokens) - 1] >> 32) == id && before > 0;
+        const unsigned on = __ballot_sync(0xffffffffu, goes_on);
+        const unsigned back = __ballot_sync(0xffffffffu, came);
+        if ((on != ~0u) & (back != ~0u)) {
+            first = piece - (__ffs(~back) - 1);
+            last = piece + (__ffs(~on) - 1);
+            return;
+        }
         const uint64_t bounds[2] = {(uint64_t)id << 32, (uint64_t)(id + 1) << 32};
-        int at[2];
-        warp_count_below(k.keys, (int)p.tokens, bounds, at, lane);
-        const int64_t first = at[0] / k.piece, last = (at[1] - 1) / k.piece;
-        const int64_t from = max(first, piece / JOIN * JOIN);
-        const int64_t to = min(last, piece / JOIN * JOIN + JOIN - 1);
-        const int64_t pieces = k.sum_items / k.panels;
+        int place[2];
+        warp_count_below(k.keys, (int)p.tokens, bounds, place, lane);
+        first = place[0] >> k.piece_log;
+        last = (place[1] - 1) >> k.piece_log;
+    }
+    // This piece's part of the run of `id` is kept: the last to come here joins the parts.
+    __device__ void join(int piece, unsigned id, int panel) {
+        int first, last;
+        run_pieces(piece, id, first, last);
+        const int from = max(first, piece / JOIN * JOIN);
+        const int to = min(last, piece / JOIN * JOIN + JOIN - 1);
+        const int64_t pieces = k.pieces;
         // a piece begins one run and may continue another: two counters
         if (!last_of((from == first ? pieces : 0) + from, panel, to - from + 1)) return;
         lead = lead_for(id);
         add_partials(from, to, 1, first);
         if (first / JOIN != last / JOIN) {
-            float* sum = partial(2 * from + (from == first));
+            float* sum = partial(2 * (int64_t)from + (from == first));
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (inside(v)) store_vec<Cache::KEEP, float, W>(sum + column(v, 0), acc[v]);
             if (!last_of(2 * pieces + first, panel, last / JOIN - first / JOIN + 1)) return;
             // the first group's sum is at `first`, the others' at their first pieces
             add_partials((first / JOIN + 1) * JOIN, last, JOIN, first);
-            const float* part = partial(2 * first + 1);
+            const float* part = partial(2 * (int64_t)first + 1);
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -542,18 +574,22 @@ struct GradSum {
         finish(id);
     }
 
-    __device__ void sum(int64_t piece, int panel) {
+    __device__ void sum(int piece, int panel) {
         const T* dout = static_cast<const T*>(p.dout);
         const int64_t elements = (p.tokens - 1) * p.ld_dout + p.dim;
-        const int s0 = (int)(piece * k.piece);
-        const int s1 = (int)min((int64_t)s0 + k.piece, p.tokens);
-        unsigned run = (unsigned)(k.keys[s0] >> 32);            // the id being summed
+        const int s0 = piece << k.piece_log;
+        const int s1 = (int)min((int64_t)s0 + (1 << k.piece_log), p.tokens);
+        // the first keys, the one before and the one behind (which is there always), all
+        // on their way together
+        uint64_t mine = k.keys[min(s0 + lane, s1 - 1)];
+        const uint64_t key_before = k.keys[max(s0 - 1, 0)], key_behind = k.keys[s1];
+        unsigned run = (unsigned)(__shfl_sync(0xffffffffu, mine, 0) >> 32);   // the id being summed
         if (run == NO_ID) return;
-        bool from_before = s0 > 0 && (unsigned)(k.keys[s0 - 1] >> 32) == run;
+        bool from_before = s0 > 0 && (unsigned)(key_before >> 32) == run;
         unsigned head = NO_ID;                                  // a run from before that ended
         begin(run);
         for (int base = s0; base < s1; base += 32) {
-            const uint64_t mine = k.keys[min(base + lane, s1 - 1)];
+            if (base > s0) mine = k.keys[min(base + lane, s1 - 1)];
             const unsigned pos_l = (unsigned)mine;
             const unsigned id_l = base + lane < s1 ? (unsigned)(mine >> 32) : NO_ID;
             const int live = __popc(__ballot_sync(0xffffffffu, id_l != NO_ID));  // a prefix
@@ -629,7 +665,7 @@ struct GradSum {
             }
             if (live < 32) break;
         }
-        const bool goes_on = s1 < p.tokens && (unsigned)(k.keys[s1] >> 32) == run;
+        const bool goes_on = s1 < p.tokens && (unsigned)(key_behind >> 32) == run;
         const bool crosses = from_before || goes_on;
         if (crosses) leave_partial(piece, from_before);
         else finish(run);
@@ -692,9 +728,12 @@ __global__ __launch_bounds__(256, 3) void grad_sums(EmbedGradParams p, GradWork 
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (item < k.sum_items) {
-        const int panel = (int)(item % k.panels);
+        // a division of 32 bits where it will do
+        const int piece = (int)(item <= UINT_MAX ? (unsigned)item / (unsigned)k.panels
+                                                 : item / k.panels);
+        const int panel = (int)(item - (int64_t)piece * k.panels);
         GradSum<T, G, W, V, BATCH, EDGES> s{p, k, lane, panel * PANEL, (int)p.dim};
-        s.sum(item / k.panels, panel);
+        s.sum(piece, panel);
     } else {
         const int64_t fill = item - k.sum_items;
         if (fill * k.fill_rows < p.vocab) fill_rows<G, EDGES>(p, k, fill, lane);
@@ -711,8 +750,7 @@ struct GradLayout {
 };
 GradLayout grad_layout(int64_t tokens, int64_t dim) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const int piece = piece_of(tokens, dim);
-    const size_t pieces = (size_t)((tokens + piece - 1) / piece);
+    const size_t pieces = (size_t)pieces_of(tokens, piece_log_of(tokens, dim));
     GradLayout l{};
     l.other = up(key_bytes(tokens));
     l.arrived = l.other + up(key_bytes(tokens));
@@ -758,14 +796,15 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
     k.arrived = reinterpret_cast<int*>(scratch + l.arrived);
     k.partials = reinterpret_cast<float*>(scratch + l.partials);
     k.dim_padded = padded(p.dim);
-    k.piece = piece_of(p.tokens, p.dim);
+    k.piece_log = piece_log_of(p.tokens, p.dim);
+    k.pieces = (int)pieces_of(p.tokens, k.piece_log);
     const int W = 16 / lm_elem_size(type);
     const bool whole = p.dim % W == 0 &&
                        rows_aligned16(p.dtable, p.ld_dtable, lm_elem_size(grad_type)) &&
                        (p.tokens == 0 || rows_aligned16(p.dout, p.ld_dout, lm_elem_size(type)));
     // a row between boundaries covers up to W - 1 columns more
     k.panels = (int)panels_of(p.dim + (whole ? 0 : W - 1));
-    k.sum_items = (p.tokens + k.piece - 1) / k.piece * k.panels;
+    k.sum_items = (int64_t)k.pieces * k.panels;
     // a filling warp writes about 32 KB when no row of its share has a token
     const int64_t row_bytes = p.dim * lm_elem_size(grad_type);
     k.fill_rows = (int)std::min<int64_t>(32, std::max<int64_t>(1, 32768 / row_bytes));
@@ -779,7 +818,7 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
         const unsigned total = (unsigned)tiles * SORT_TILE;
         for (int64_t run = SORT_TILE; e == cudaSuccess && run < total;) {
             const int64_t runs = (total + run - 1) / run;
-            const int ways = runs <= 4 ? 4 : runs <= 8 ? 8 : MERGE_WAYS;
+            const int ways = runs <= 4 || total > MERGE_MANY ? 4 : runs <= 8 ? 8 : MERGE_WAYS;
             auto kernel = ways == 4 ? merge_runs<4> : ways == 8 ? merge_runs<8> : merge_runs<16>;
             e = launch_chained(kernel, dim3(total / 32), dim3(32 * ways), 0, st, true,
                                (const uint64_t*)keys, other, total, (unsigned)run);
