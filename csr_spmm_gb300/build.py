@@ -1,8 +1,9 @@
 """Build the CUDA library ``csr_spmm_gb300/lib/libcsrspmm.so`` for sm_103a.
 
 Each translation unit under ``csrc/`` is compiled by its own nvcc process
-(in parallel), then the objects are linked into one shared library with the
-CUDA runtime linked statically.  A rebuild happens only when a source,
+(in parallel), then the objects are linked into one shared library on the shared
+CUDA runtime.  Beside it g++ builds ``_torch_outputs.so``, the module that makes the
+torch wrappers' output tensors.  A rebuild happens only when a source,
 header or flag changed (a content hash is kept beside the library).
 
 Run ``python -m csr_spmm_gb300.build`` or call :func:`build`.
@@ -10,10 +11,12 @@ Run ``python -m csr_spmm_gb300.build`` or call :func:`build`.
 from __future__ import annotations
 
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libcsrspmm.so")
+TORCH_OUTPUTS = os.path.join(LIB_DIR, "_torch_outputs.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC",
@@ -43,6 +47,40 @@ def _runtime_path(nvcc: str) -> list:
     """Where the library finds libcudart when no one in the process has loaded it."""
     lib = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "lib64")
     return ["-Xlinker", "-rpath," + lib] if os.path.isdir(lib) else []
+
+
+def _torch_outputs(force: bool = False) -> None:
+    """The torch wrappers' own module (host code; nothing without torch)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return
+    torch = list(spec.submodule_search_locations)[0]
+    src = os.path.join(CSRC, "torch_outputs.cpp")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [os.path.join(torch, "include"), sysconfig.get_paths()["include"],
+               os.path.join(cuda, "include")]
+    libs = os.path.join(torch, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", src]
+    cmd += [f for i in include for f in ("-isystem", i)]
+    cmd += ["-L" + libs, "-Wl,-rpath," + libs]
+    cmd += ["-l" + lib for lib in ("torch_python", "torch_cuda", "torch_cpu", "c10")]
+    h = hashlib.sha256(" ".join(cmd).encode())
+    for name in (src, os.path.join(torch, "version.py")):
+        with open(name, "rb") as f:
+            h.update(f.read())
+    stamp = TORCH_OUTPUTS + ".sha256"
+    if not force and os.path.exists(TORCH_OUTPUTS) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == h.hexdigest():
+                return
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = TORCH_OUTPUTS + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_outputs.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_OUTPUTS)
+    with open(stamp, "w") as f:
+        f.write(h.hexdigest() + "\n")
 
 
 def _sources():
@@ -86,6 +124,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), out: str =
     if not force and os.path.exists(out) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == digest:
+                if out == LIB:
+                    _torch_outputs()
                 return out
     nvcc = _nvcc()
     os.makedirs(obj_dir, exist_ok=True)
@@ -106,7 +146,10 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), out: str =
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(units), os.cpu_count() or 4))) as ex:
+        outputs = ex.submit(_torch_outputs, force) if out == LIB else None
         objs = list(ex.map(compile_one, units))
+        if outputs is not None:
+            outputs.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + LINK_FLAGS + _runtime_path(nvcc) + ["-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

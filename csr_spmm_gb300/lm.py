@@ -11,6 +11,9 @@ the stream has used it.
 """
 from __future__ import annotations
 
+import importlib.util
+import os
+
 import torch
 
 from . import _lib
@@ -18,6 +21,7 @@ from . import _lib
 _TYPES = {torch.float32: _lib.SPMM_F32, torch.float16: _lib.SPMM_F16,
           torch.bfloat16: _lib.SPMM_BF16}
 _F32, _I32 = torch.float32, torch.int32
+_INDEX = 3                               # beside the library's type codes: int32
 
 # Small calls are bound by this file (a kernel of 2 us behind 10 us of Python), so
 # each check reads a tensor's attributes once and nothing is built on the way.
@@ -68,12 +72,32 @@ def _current(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _new(shape, dtype, device: int, stream):
-    """A tensor for an output, allocated for the stream that writes it."""
+def _outputs():
+    """The compiled module that makes output tensors (csrc/torch_outputs.cpp)."""
+    path = os.path.join(_lib.PKG, "lib", "_torch_outputs.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing. Run `python -m csr_spmm_gb300.build`.")
+    spec = importlib.util.spec_from_file_location("_torch_outputs", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_make = None
+
+
+def _new(stream, device: int, *what):
+    """Tensors for outputs, allocated for the stream that writes them: `what` is a type
+    code, rows and columns for each, columns < 0 for a vector.
+
+    All of a call's at once and compiled: AAAA."""
+    global _make
+    if _make is None:
+        _make = _outputs().new
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _make(device, *what)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _make(device, *what)
 
 
 def _enter(device: int, stream, tensors) -> int:
@@ -113,7 +137,7 @@ def embedding(handle, ids, table, scale: float = 1.0, out=None, stream=None):
     a_ids, a_table = _address(ids, device), _address(table, device)
     st = _enter(device, stream, (ids, table, out))
     if out is None:
-        out = _new((n, dim), table.dtype, device, stream)
+        out, = _new(stream, device, code, n, dim)
     _lib.spmm_embedding(handle.ptr, code, scale, a_ids, n, a_table, ld, vocab, dim,
                         _address(out, device), ld_out, st)
     return out
@@ -175,8 +199,9 @@ def layer_norm(handle, x, weight=None, bias=None, eps: float = 1e-5, out=None, s
     a_x, a_w, a_b = _address(x, device), _address(weight, device), _address(bias, device)
     st = _enter(device, stream, (x, weight, bias, out))
     if out is None:
-        out = _new((rows, dim), x.dtype, device, stream)
-    mean, rstd = _new(rows, _F32, device, stream), _new(rows, _F32, device, stream)
+        out, mean, rstd = _new(stream, device, code, rows, dim, 0, rows, -1, 0, rows, -1)
+    else:
+        mean, rstd = _new(stream, device, 0, rows, -1, 0, rows, -1)
     _lib.spmm_layer_norm(handle.ptr, code, param_code, a_x, ld, rows, dim, a_w, a_b, eps,
                          _address(out, device), ld_y, mean.data_ptr(), rstd.data_ptr(), st)
     return out, mean, rstd
@@ -207,16 +232,19 @@ def layer_norm_grad(handle, dy, x, mean, rstd, weight=None, bias: bool = True, o
     a_dy, a_x, a_w = _address(dy, device), _address(x, device), _address(weight, device)
     a_mean, a_rstd = _address(mean, device), _address(rstd, device)
     st = _enter(device, stream, (dy, x, mean, rstd, weight, out))
+    what = ((code, rows, dim) if out is None else ()) + \
+        ((param_code, dim, -1) if weight is not None else ()) + \
+        ((param_code, dim, -1) if bias else ())
+    made = iter(_new(stream, device, *what))
     if out is None:
-        out = _new((rows, dim), x.dtype, device, stream)
-    pt = x.dtype if weight is None else weight.dtype
+        out = next(made)
     dweight = dbias = None
     a_dw = a_db = 0
     if weight is not None:
-        dweight = _new(dim, pt, device, stream)
+        dweight = next(made)
         a_dw = dweight.data_ptr()
     if bias:
-        dbias = _new(dim, pt, device, stream)
+        dbias = next(made)
         a_db = dbias.data_ptr()
     _lib.spmm_layer_norm_grad(handle.ptr, code, param_code, a_dy, ld_dy, a_x, ld, a_mean, a_rstd,
                               a_w, rows, dim, _address(out, device), ld_dx, a_dw, a_db, st)
@@ -240,15 +268,18 @@ def token_logprob(handle, logits, targets=None, alpha: float = 1.0, top: int = 0
     device = handle.device
     a_x, a_t = _address(logits, device), _address(targets, device)
     st = _enter(device, stream, (logits, targets))
-    entropy, lse = _new(rows, _F32, device, stream), _new(rows, _F32, device, stream)
+    # entropy, lse, logprob
+    what = (0, rows, -1) * (2 if targets is None else 3)
+    if top:
+        what += (0, rows, top, _INDEX, rows, top)
+    entropy, lse, *made = _new(stream, device, *what)
     logprob = top_logprob = top_index = None
     a_lp = a_tl = a_ti = 0
     if targets is not None:
-        logprob = _new(rows, _F32, device, stream)
+        logprob = made[0]
         a_lp = logprob.data_ptr()
     if top:
-        top_logprob = _new((rows, top), _F32, device, stream)
-        top_index = _new((rows, top), _I32, device, stream)
+        top_logprob, top_index = made[-2:]
         a_tl, a_ti = top_logprob.data_ptr(), top_index.data_ptr()
     _lib.spmm_token_logprob(handle.ptr, code, alpha, a_x, ld, rows, vocab, a_t, top, a_lp,
                             entropy.data_ptr(), lse.data_ptr(), a_tl, a_ti, st)
@@ -290,7 +321,7 @@ def token_logprob_grad(handle, logits, targets, lse, entropy=None, dlogprob=None
                          _address(dentropy, device))
     st = _enter(device, stream, (logits, targets, lse, entropy, dlogprob, dentropy, out))
     if out is None:
-        out = _new((rows, vocab), logits.dtype, device, stream)
+        out, = _new(stream, device, code, rows, vocab)
     _lib.spmm_token_logprob_grad(handle.ptr, code, alpha, a_x, ld, rows, vocab, a_t, a_lse, a_ent,
                                  a_dl, a_de, _address(out, device), ld_out, st)
     return out
