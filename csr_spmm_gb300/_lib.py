@@ -9,6 +9,7 @@ no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -382,12 +383,38 @@ def spmm_reserve_lm(handle, rows, dim) -> None:
     _check(library().spmm_reserve_lm(handle, rows, dim), "spmm_reserve_lm")
 
 
+def load_module(name: str):
+    """A compiled Python module built beside the library."""
+    path = os.path.join(PKG, "lib", name + ".so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing. Run `python -m csr_spmm_gb300.build` "
+                          "(or __graft_entry__.build()).")
+    spec = importlib.util.spec_from_file_location(name, path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_calls = None
+
+
+def _bind_calls():
+    """The compiled calls of the functions below, on this library (made once)."""
+    global _calls
+    lib, module = library(), load_module("_lm_calls")
+    module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        lib.spmm_embedding, lib.spmm_embedding_grad, lib.spmm_layer_norm,
+        lib.spmm_layer_norm_grad, lib.spmm_token_logprob, lib.spmm_token_logprob_grad)))
+    _calls = module
+    return module
+
+
 def spmm_embedding(handle, type_, scale, ids, tokens, table, ld_table, vocab, dim, out, ld_out,
                    stream=0, check=True) -> int:
     """out[t, :] = scale * table[ids[t], :] (device pointers, spmm_type_t)."""
-    s = library().spmm_embedding(handle, type_, scale, ids, tokens, table, ld_table, vocab, dim,
-                                 out, ld_out, stream or None)
-    if check:
+    s = (_calls or _bind_calls()).spmm_embedding(handle, type_, scale, ids, tokens, table, ld_table,
+                                                 vocab, dim, out, ld_out, stream)
+    if s and check:
         _check(s, "spmm_embedding")
     return s
 
@@ -395,9 +422,10 @@ def spmm_embedding(handle, type_, scale, ids, tokens, table, ld_table, vocab, di
 def spmm_embedding_grad(handle, type_, grad_type, scale, ids, tokens, dout, ld_dout, beta, dtable,
                         ld_dtable, vocab, dim, stream=0, check=True) -> int:
     """dtable = beta * dtable + the gradient of spmm_embedding."""
-    s = library().spmm_embedding_grad(handle, type_, grad_type, scale, ids, tokens, dout, ld_dout,
-                                      beta, dtable, ld_dtable, vocab, dim, stream or None)
-    if check:
+    s = (_calls or _bind_calls()).spmm_embedding_grad(handle, type_, grad_type, scale, ids, tokens,
+                                                      dout, ld_dout, beta, dtable, ld_dtable, vocab,
+                                                      dim, stream)
+    if s and check:
         _check(s, "spmm_embedding_grad")
     return s
 
@@ -405,9 +433,9 @@ def spmm_embedding_grad(handle, type_, grad_type, scale, ids, tokens, dout, ld_d
 def spmm_layer_norm(handle, type_, param_type, x, ldx, rows, dim, weight, bias, eps, y, ldy, mean,
                     rstd, stream=0, check=True) -> int:
     """y = (x - mean) * rstd * weight + bias for each row; mean and rstd are outputs."""
-    s = library().spmm_layer_norm(handle, type_, param_type, x, ldx, rows, dim, weight, bias, eps,
-                                  y, ldy, mean, rstd, stream or None)
-    if check:
+    s = (_calls or _bind_calls()).spmm_layer_norm(handle, type_, param_type, x, ldx, rows, dim,
+                                                  weight, bias, eps, y, ldy, mean, rstd, stream)
+    if s and check:
         _check(s, "spmm_layer_norm")
     return s
 
@@ -415,10 +443,10 @@ def spmm_layer_norm(handle, type_, param_type, x, ldx, rows, dim, weight, bias, 
 def spmm_layer_norm_grad(handle, type_, param_type, dy, ld_dy, x, ldx, mean, rstd, weight, rows,
                          dim, dx, ld_dx, dweight, dbias, stream=0, check=True) -> int:
     """Gradients of spmm_layer_norm with respect to x, weight and bias."""
-    s = library().spmm_layer_norm_grad(handle, type_, param_type, dy, ld_dy, x, ldx, mean, rstd,
-                                       weight, rows, dim, dx, ld_dx, dweight, dbias,
-                                       stream or None)
-    if check:
+    s = (_calls or _bind_calls()).spmm_layer_norm_grad(handle, type_, param_type, dy, ld_dy, x, ldx,
+                                                       mean, rstd, weight, rows, dim, dx, ld_dx,
+                                                       dweight, dbias, stream)
+    if s and check:
         _check(s, "spmm_layer_norm_grad")
     return s
 
@@ -426,10 +454,10 @@ def spmm_layer_norm_grad(handle, type_, param_type, dy, ld_dy, x, ldx, mean, rst
 def spmm_token_logprob(handle, type_, alpha, logits, ld, rows, vocab, targets, top_k, logprob,
                        entropy, lse, top_logprob, top_index, stream=0, check=True) -> int:
     """Per row of logits: log probability of the target, entropy, log-sum-exp, alternatives."""
-    s = library().spmm_token_logprob(handle, type_, alpha, logits, ld, rows, vocab, targets,
-                                     top_k, logprob, entropy, lse, top_logprob, top_index,
-                                     stream or None)
-    if check:
+    s = (_calls or _bind_calls()).spmm_token_logprob(handle, type_, alpha, logits, ld, rows, vocab,
+                                                     targets, top_k, logprob, entropy, lse,
+                                                     top_logprob, top_index, stream)
+    if s and check:
         _check(s, "spmm_token_logprob")
     return s
 
@@ -437,9 +465,9 @@ def spmm_token_logprob(handle, type_, alpha, logits, ld, rows, vocab, targets, t
 def spmm_token_logprob_grad(handle, type_, alpha, logits, ld, rows, vocab, targets, lse, entropy,
                             dlogprob, dentropy, dlogits, ld_dlogits, stream=0, check=True) -> int:
     """Gradient of the log probabilities and entropies with respect to the logits."""
-    s = library().spmm_token_logprob_grad(handle, type_, alpha, logits, ld, rows, vocab, targets,
-                                          lse, entropy, dlogprob, dentropy, dlogits, ld_dlogits,
-                                          stream or None)
-    if check:
+    s = (_calls or _bind_calls()).spmm_token_logprob_grad(handle, type_, alpha, logits, ld, rows,
+                                                          vocab, targets, lse, entropy, dlogprob,
+                                                          dentropy, dlogits, ld_dlogits, stream)
+    if s and check:
         _check(s, "spmm_token_logprob_grad")
     return s

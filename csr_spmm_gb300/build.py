@@ -2,8 +2,9 @@
 
 Each translation unit under ``csrc/`` is compiled by its own nvcc process
 (in parallel), then the objects are linked into one shared library on the shared
-CUDA runtime.  Beside it g++ builds ``_torch_outputs.so``, the module that makes the
-torch wrappers' output tensors.  A rebuild happens only when a source,
+CUDA runtime.  Beside it g++ builds two Python modules for short calls: ``_lm_calls.so``
+calls the language-model entry points, ``_torch_outputs.so`` makes the torch wrappers'
+output tensors.  A rebuild happens only when a source,
 header or flag changed (a content hash is kept beside the library).
 
 Run ``python -m csr_spmm_gb300.build`` or call :func:`build`.
@@ -26,7 +27,6 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libcsrspmm.so")
-TORCH_OUTPUTS = os.path.join(LIB_DIR, "_torch_outputs.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC",
@@ -49,38 +49,47 @@ def _runtime_path(nvcc: str) -> list:
     return ["-Xlinker", "-rpath," + lib] if os.path.isdir(lib) else []
 
 
-def _torch_outputs(force: bool = False) -> None:
-    """The torch wrappers' own module (host code; nothing without torch)."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
-        return
-    torch = list(spec.submodule_search_locations)[0]
-    src = os.path.join(CSRC, "torch_outputs.cpp")
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
-    include = [os.path.join(torch, "include"), sysconfig.get_paths()["include"],
-               os.path.join(cuda, "include")]
-    libs = os.path.join(torch, "lib")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", src]
-    cmd += [f for i in include for f in ("-isystem", i)]
-    cmd += ["-L" + libs, "-Wl,-rpath," + libs]
-    cmd += ["-l" + lib for lib in ("torch_python", "torch_cuda", "torch_cpu", "c10")]
+def _module(name: str, deps, flags, libs, force: bool) -> None:
+    """Build csrc/<name>.cpp, a Python module, with the host compiler."""
+    src, out = os.path.join(CSRC, name + ".cpp"), os.path.join(LIB_DIR, "_" + name + ".so")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", src, "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"]] + flags + libs
     h = hashlib.sha256(" ".join(cmd).encode())
-    for name in (src, os.path.join(torch, "version.py")):
-        with open(name, "rb") as f:
+    for dep in [src] + deps:
+        with open(dep, "rb") as f:
             h.update(f.read())
-    stamp = TORCH_OUTPUTS + ".sha256"
-    if not force and os.path.exists(TORCH_OUTPUTS) and os.path.exists(stamp):
+    stamp = out + ".sha256"
+    if not force and os.path.exists(out) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == h.hexdigest():
                 return
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = TORCH_OUTPUTS + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on torch_outputs.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TORCH_OUTPUTS)
+        raise RuntimeError(f"g++ failed on {name}.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
     with open(stamp, "w") as f:
         f.write(h.hexdigest() + "\n")
+
+
+def _lm_calls(force: bool = False) -> None:
+    """The module that calls the language-model entry points."""
+    _module("lm_calls", [os.path.join(INCLUDE, "csr_spmm.h")], [], [], force)
+
+
+def _torch_outputs(force: bool = False) -> None:
+    """The module that makes the torch wrappers' outputs (none without torch)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return
+    torch = list(spec.submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    libs = os.path.join(torch, "lib")
+    _module("torch_outputs", [os.path.join(torch, "version.py")],
+            ["-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include")],
+            ["-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+             "-lc10"], force)
 
 
 def _sources():
@@ -125,6 +134,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), out: str =
         with open(stamp) as f:
             if f.read().strip() == digest:
                 if out == LIB:
+                    _lm_calls()
                     _torch_outputs()
                 return out
     nvcc = _nvcc()
@@ -146,10 +156,10 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), out: str =
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(units), os.cpu_count() or 4))) as ex:
-        outputs = ex.submit(_torch_outputs, force) if out == LIB else None
+        modules = [ex.submit(m, force) for m in (_torch_outputs, _lm_calls) if out == LIB]
         objs = list(ex.map(compile_one, units))
-        if outputs is not None:
-            outputs.result()
+        for m in modules:
+            m.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + LINK_FLAGS + _runtime_path(nvcc) + ["-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

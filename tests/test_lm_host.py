@@ -147,6 +147,36 @@ def test_calls_pass_addresses_and_leading_dimensions(monkeypatch):
     assert calls == []
 
 
+def test_compiled_calls_convert_their_arguments(lib):
+    """The raw functions: numbers and addresses as the C signature has them, or an error."""
+    inv = cs.SPMM_ERR_INVALID_ARGUMENT
+    assert _lib.spmm_embedding(None, 0, 1, 0, 4, None, 4, 4, 4, 0, 4, 0, check=False) == inv
+    with pytest.raises(cs.SpmmError, match="spmm_layer_norm"):
+        _lib.spmm_layer_norm(None, 0, 0, 0, 4, 4, 4, 0, 0, 0.0, 0, 4, 0, 0)
+    calls = _lib.load_module("_lm_calls")
+    with pytest.raises(TypeError, match="12 arguments"):
+        calls.spmm_embedding(0)
+    with pytest.raises(TypeError):
+        _lib.spmm_embedding("h", 0, 1.0, 0, 4, 0, 4, 4, 4, 0, 4)
+    with pytest.raises(TypeError):
+        _lib.spmm_embedding(0, 0, "1.0", 0, 4, 0, 4, 4, 4, 0, 4)
+    with pytest.raises(OverflowError):
+        _lib.spmm_embedding(0, 0, 1.0, 0, 1 << 63, 0, 4, 4, 4, 0, 4)
+    with pytest.raises(ImportError, match="is missing"):
+        _lib.load_module("_no_such_module")
+
+
+def test_outputs_are_refused_in_other_forms(lib):
+    new = _lib.load_module("_torch_outputs").new
+    with pytest.raises(TypeError, match="type, rows, columns"):
+        new(0, 0, 4)
+    assert new(0) == ()
+    with pytest.raises(ValueError, match="no such type"):
+        new(0, 4, 1, 1)
+    with pytest.raises(TypeError):
+        new(0, 0, "1", 1)
+
+
 def test_the_package_imports_without_torch():
     """torch is needed by the tensor wrappers only, and loaded on their first use."""
     import subprocess
