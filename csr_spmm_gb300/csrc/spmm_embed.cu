@@ -219,8 +219,8 @@ cudaError_t launch_embed(const EmbedParams& p, bool whole, int num_sms, cudaStre
 constexpr int SORT_TILE = 512;       // keys sorted by one block, one per thread
 constexpr int MERGE_WAYS = 16;       // sorted runs merged per round, at most
 // From so many keys on the searches cost more than the launches they save, and fours
-// merged round by round have the fewest: 300,000 tokens of 64 columns take 135 us, with 16
-// runs to a round 167; 65,536 tokens the same either way.
+// merged round by round have the fewest: 300,000 tokens of 64 columns take 134 us, with 16
+// runs to a round 167 and with 8 168; 65,536 tokens the same either way.
 constexpr unsigned MERGE_MANY = 32768;
 constexpr unsigned NO_ID = 0xfffffffdu;  // of padding tokens
 constexpr unsigned REST = 0xfffffffeu;   // behind them, what fills the last tile
@@ -287,8 +287,8 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
 // A block takes 32 consecutive keys, a warp of it one of the runs: its lanes search
 // for neighbouring keys, so their probes share memory words, and a search is one chain
 // of loads with many others beside it: 8192 keys 5 us (one thread per key with WAYS
-// chains: 25 us, its loads waiting for one another), 65,536 in two rounds 22 us.  Behind the `total` keys (whole tiles) lies a largest one, which ends every
-// search that would go further.
+// chains: 25 us, its loads waiting for one another).  Behind the `total` keys (whole
+// tiles) lies a largest one, which ends every search that would go further.
 template <int WAYS>
 __global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restrict__ in,
                                                         uint64_t* __restrict__ out,
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restri
 // the last of those sums to arrive adds them in order: a token that makes up a
 // tenth of 300,000 has near a thousand pieces.  Warps behind those of the sums write the
 // rows without a token.  The bound is HBM: 65,536 tokens of 4096 bf16 into a table of
-// 131,072 binary32 rows take 409 us with the sort, 6.5 TB/s of what must move (96% of
+// 131,072 binary32 rows take 407 us with the sort, 6.5 TB/s of what must move (97% of
 // the copy rate).  80 registers for three blocks per SM (some spill in the joins): 414 us
 // with 99 and two, and where rows are added to instead of written 294 us against 252.
 constexpr int PANEL = 256;           // columns per warp: 512 bytes of a 16-bit row

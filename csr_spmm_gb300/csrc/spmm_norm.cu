@@ -390,8 +390,8 @@ constexpr int GRAD_STAGES = sizeof(T) == 4 ? 3 : 4;
 // dy * xhat and dy in registers to the end.  GIVEN: rows of more than GRAD_COLUMNS
 // columns, in tiles of as many (blockIdx.y); the row's two means come from
 // grad_means and nothing is exchanged.  The bound is HBM (read dy and x, write dx):
-// 32,768 rows of 4096 bf16 142 us with the join, 5.7 TB/s (84% of the copy rate), 30,000
-// binary32 rows of 4096 240 us (91%).  128 registers hold the sums, which leaves 16 warps
+// 32,768 rows of 4096 bf16 138 us with the join, 5.8 TB/s (86% of the copy rate), 30,000
+// binary32 rows of 4096 239 us (91%).  128 registers hold the sums, which leaves 16 warps
 // per SM; 64 or 80 registers spill and take 220 us or more.
 // part: [slices, or blocks of narrow rows][2][dim].
 template <typename T, typename P, int W, int K, Fit FIT, bool GIVEN>
@@ -641,7 +641,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void norm_grad_rows(NormGradParams p,
 
 // The two means of each row: a block per row.  W == 1 where x and dy lie differently
 // against 16-byte boundaries.  Wide rows read dy and x twice so: 18,000 of 16,384 bf16
-// take 490 us, 5 passes over memory where 3 are needed (261 us).
+// take 482 us, 5 passes over memory where 3 are needed (261 us).
 template <typename T, typename P, int W>
 __global__ __launch_bounds__(ANY_THREADS) void grad_means(NormGradParams p) {
     __shared__ float s[ANY_THREADS / 32];

@@ -20,7 +20,7 @@ _TYPES = {torch.float32: _lib.SPMM_F32, torch.float16: _lib.SPMM_F16,
 _F32, _I32 = torch.float32, torch.int32
 _INDEX = 3                               # beside the library's type codes: int32
 
-# Small calls are bound by this file (a kernel of 2 us behind 10 us of Python), so
+# Small calls are bound by this file (a kernel of 2 us behind 6 us of host code), so
 # each check reads a tensor's attributes once and nothing is built on the way.
 
 
