@@ -10,11 +10,14 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <array>
+#include <pybind11/gil.h>
+
 #include <optional>
+#include <utility>
 
 namespace {
 
+constexpr int MOST = 8;               // tensors per call
 constexpr at::ScalarType TYPES[] = {at::kFloat, at::kHalf, at::kBFloat16, at::kInt};
 
 PyObject* make(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -23,32 +26,36 @@ PyObject* make(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_SetString(PyExc_TypeError, "new(device, [type, rows, columns]...)");
         return nullptr;
     }
-    const at::Device device(at::kCUDA, static_cast<at::DeviceIndex>(PyLong_AsLong(args[0])));
-    PyObject* all = PyTuple_New(n / 3);
-    if (!all) return nullptr;
-    for (Py_ssize_t i = 0; i < n / 3; ++i) {
-        const long type = PyLong_AsLong(args[3 * i + 1]);
-        const std::array<int64_t, 2> sizes{PyLong_AsLongLong(args[3 * i + 2]),
-                                           PyLong_AsLongLong(args[3 * i + 3])};
-        if (PyErr_Occurred() || type < 0 || type > 3) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no such type");
-            Py_DECREF(all);
-            return nullptr;
-        }
-        at::Tensor t;
-        try {
-            t = at::detail::empty_cuda(at::IntArrayRef(sizes.data(), sizes[1] < 0 ? 1 : 2),
-                                       TYPES[type], device, std::nullopt);
-        } catch (...) {
-            Py_DECREF(all);
-            throw;
-        }
-        PyObject* one = THPVariable_Wrap(std::move(t));
-        if (!one) {
-            Py_DECREF(all);
-            return nullptr;
-        }
-        PyTuple_SET_ITEM(all, i, one);
+    const Py_ssize_t count = n / 3;
+    if (count > MOST) {
+        PyErr_Format(PyExc_TypeError, "at most %d tensors", MOST);
+        return nullptr;
+    }
+    const long index = PyLong_AsLong(args[0]);
+    long types[MOST];
+    int64_t sizes[MOST][2];
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        types[i] = PyLong_AsLong(args[3 * i + 1]);
+        for (int k = 0; k < 2; ++k) sizes[i][k] = PyLong_AsLongLong(args[3 * i + 2 + k]);
+        if (!PyErr_Occurred() && (types[i] < 0 || types[i] > 3))
+            PyErr_SetString(PyExc_ValueError, "no such type");
+        if (PyErr_Occurred()) return nullptr;
+    }
+    if (PyErr_Occurred()) return nullptr;
+    const at::Device device(at::kCUDA, static_cast<at::DeviceIndex>(index));
+    at::Tensor made[MOST];
+    {
+        // an allocation may wait for the device, whose callbacks may wait for Python
+        pybind11::gil_scoped_release released;
+        for (Py_ssize_t i = 0; i < count; ++i)
+            made[i] = at::detail::empty_cuda(at::IntArrayRef(sizes[i], sizes[i][1] < 0 ? 1 : 2),
+                                             TYPES[types[i]], device, std::nullopt);
+    }
+    PyObject* all = PyTuple_New(count);
+    for (Py_ssize_t i = 0; all && i < count; ++i) {
+        PyObject* one = THPVariable_Wrap(std::move(made[i]));
+        if (one) PyTuple_SET_ITEM(all, i, one);
+        else Py_CLEAR(all);
     }
     return all;
     END_HANDLE_TH_ERRORS
