@@ -21,6 +21,7 @@ namespace cg = cooperative_groups;
 constexpr unsigned ALL = 0xffffffffu;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LARGEST = 3.402823466e38f;
 
 // ---- small pieces ---------------------------------------------------------------
 
@@ -172,6 +173,13 @@ __device__ __forceinline__ Sums join(Sums a, float c, float low) {
     return {m, warp_sum(a.s), warp_sum(a.u)};
 }
 
+// Log probability of a logit, alpha x - lse in one rounding.  alpha x counts in binary32: a
+// logit that alpha takes below its range is masked, whatever lse would make of it.
+__device__ __forceinline__ float log_p(float alpha, float x, float lse) {
+    const float z = __fmul_rn(alpha, x);
+    return z == -INFINITY ? z - lse : fmaf(alpha, x, -lse);
+}
+
 struct RowShared {
     Sums sums[LP_WARPS];
     Sums total;                                 // this block's part of the row
@@ -203,7 +211,7 @@ __device__ void collect(RowShared& sh, const Row<T>& row, const Part& part, int 
                         unsigned least) {
     constexpr int W = Row<T>::W;
     // in values: NaN and -inf compare false, and what is no number's order means all
-    const float from = least > 0x00800000u ? value_of(least) : -3.402823466e38f;
+    const float from = least > 0x00800000u ? value_of(least) : -LARGEST;
     const int own = (int)part.turns();              // accesses of a group, at most
     const int all = chosen * own;
     for (int i0 = threadIdx.x; i0 < all; i0 += 4 * blockDim.x) {
@@ -428,7 +436,7 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
     const int64_t share = SPLIT ? (all_units + split - 1) / split : all_units;
     Part part{rank * share, 0, warps};
     part.units = max((int64_t)0, min(share, all_units - part.unit0));
-    const float c = p.alpha * LOG2E;
+    const float c = fminf(p.alpha * LOG2E, LARGEST);
     // the target's logit, wanted at the end
     const int target = tid == 0 && p.targets ? p.targets[r] : -1;
     const bool has_target = target >= 0 && target < p.vocab;
@@ -554,15 +562,16 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
         cluster.sync();
         if (rank != 0) return;
     }
-    const bool far = a.m > lim || ((a.m - low) * c < 200.0f && a.m > -INFINITY);
+    const bool far =
+        a.m > lim || (a.m > -INFINITY && ((a.m - low) * c < 200.0f || c == LARGEST));
     if (far) {
         // a maximum that the base cannot follow (+inf, huge values) or that is not far above
-        // `low` (the type's lowest value throughout): the sums again, from the differences
-        // to it
+        // `low` (the type's lowest value throughout), or a c that was cut (alpha over 2.3e38):
+        // the sums again, from the differences to it
         a.s = a.u = 0.0f;
         for (int64_t i = tid; i < p.vocab; i += blockDim.x) {
             const float v = to_f32(x[i]);
-            const float d = max_nan((v - a.m) * c, -200.0f);
+            const float d = max_nan((v - a.m) * p.alpha * LOG2E, -200.0f);
             const float q = exp2_approx(d);
             a.s += q;
             a.u = fmaf(q, d, a.u);
@@ -578,26 +587,30 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
             a.u += sh.sums[i].u;
         }
     }
-    // alpha m carries the bulk; the rest is what the base's rounding left of c m, and log2 S
-    const bool none = a.m == -INFINITY && a.s == a.s;   // nothing unmasked, and no NaN
+    // alpha m carries the bulk; the rest is what the base's rounding left of c m, and log2 S.
+    // A maximum that alpha takes beyond binary32 counts as infinite: below, the row has
+    // nothing unmasked; above, it is NaN, as a row of NaNs alone (m = -inf) is.
+    const float z = __fmul_rn(p.alpha, a.m);
+    const bool none = z == -INFINITY && a.s == a.s;      // and no NaN
+    const bool nan = !none && !(fabsf(z) < INFINITY);
     const float log_s = log2f(a.s);
     const float left = far ? 0.0f : fmaf(-a.m, c, base_of(a.m, c, low));
-    const float lse = none ? -INFINITY
-                      : a.m == -INFINITY ? NAN      // NaNs alone
-                                         : fmaf(p.alpha, a.m, LN2 * (log_s + left));
+    const float lse = none  ? -INFINITY
+                      : nan ? NAN
+                            : fmaf(p.alpha, a.m, LN2 * (log_s + left));
     if (tid == 0) {
         if (p.lse) p.lse[r] = lse;
-        if (p.entropy) p.entropy[r] = none ? 0.0f : LN2 * (log_s - a.u / a.s);
+        if (p.entropy) p.entropy[r] = none ? 0.0f : nan ? NAN : LN2 * (log_s - a.u / a.s);
         if (p.targets)
-            p.logprob[r] = !has_target ? 0.0f : none ? -INFINITY : fmaf(p.alpha, target_logit, -lse);
+            p.logprob[r] = !has_target ? 0.0f : none ? -INFINITY : log_p(p.alpha, target_logit, lse);
     }
     if (TOP && tid < p.top_k) {
         const uint64_t key = sh.best[tid];
+        const float logit = value_of((unsigned)(key >> 32));
+        const bool there = key && __fmul_rn(p.alpha, logit) > -INFINITY;
         const int64_t at = r * p.top_k + tid;
-        p.top_index[at] = key ? (int)(0xffffffffu - (unsigned)key) : -1;
-        p.top_logprob[at] = lse != lse ? NAN
-                            : key ? fmaf(p.alpha, value_of((unsigned)(key >> 32)), -lse)
-                                  : -INFINITY;
+        p.top_index[at] = there ? (int)(0xffffffffu - (unsigned)key) : -1;
+        p.top_logprob[at] = lse != lse ? NAN : there ? log_p(p.alpha, logit, lse) : -INFINITY;
     }
 }
 

@@ -1,0 +1,97 @@
+"""The language-model operators at the ends of their arguments' ranges: logits that the
+inverse temperature takes beyond binary32, and rows that hardly vary."""
+import numpy as np
+import pytest
+
+import lm_reference as ref
+from test_gpu_lm import DT, TYPES, _near, _np, cs, handle  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+LARGEST = float(np.finfo(np.float32).max)
+
+
+def _counted(x, alpha):
+    """The logits as z = alpha x in binary32 counts them: infinite where z is."""
+    with np.errstate(over="ignore"):
+        z = (np.float32(alpha) * x.astype(np.float32)).astype(np.float64)
+    return np.where(np.isinf(z), z, x)
+
+
+def _stored(value):
+    """A result as a binary32 output holds it: infinite beyond the range."""
+    return np.where(np.abs(value) > LARGEST, np.copysign(np.inf, value), value)
+
+
+def _check(cs, handle, x, targets, alpha, k):
+    """Against the definition over the counted logits; alternatives in the order of the
+    logits themselves."""
+    h_x = _np(x)
+    c_x = _counted(h_x, alpha)
+    a32 = float(np.float32(alpha))
+    want, tol = ref.token_logprob(c_x, targets, a32)
+    got = cs.token_logprob(handle, x, torch.from_numpy(targets).cuda(), alpha=alpha, top=k)
+    for g, name in zip(got[:3], ("logprob", "entropy", "lse")):
+        _near(_np(g), _stored(want[name]), tol[name], name)
+    if k:
+        index = ref.top(np.where(np.isneginf(c_x), c_x, h_x), k)
+        assert np.array_equal(got[4].cpu().numpy(), index), "top_index"
+        picked = np.take_along_axis(h_x, np.maximum(index, 0), 1)
+        lse = want["lse"][:, None]
+        with np.errstate(invalid="ignore"):
+            lp = np.where(np.isnan(lse), np.nan, np.where(index >= 0, a32 * picked - lse, -np.inf))
+            bound = tol["lse"][:, None] + ref.U * (2 * np.abs(a32 * picked) + np.abs(lp))
+        _near(_np(got[3]), _stored(lp), bound, "top_logprob")
+    up = torch.full((x.shape[0],), -1.0, device="cuda")
+    grad = cs.token_logprob_grad(handle, x, torch.from_numpy(targets).cuda(), got[2], got[1], up,
+                                 up, alpha=1.0 if alpha > 1e30 else alpha)
+    lse = want["lse"]
+    assert bool(grad[torch.from_numpy(np.isnan(lse)).cuda()].isnan().all()), "NaN rows"
+    assert not bool(grad[torch.from_numpy(np.isneginf(lse)).cuda()].any()), "empty rows"
+
+
+@pytest.mark.parametrize("times", [1, 90])
+@pytest.mark.parametrize("vocab", [9, 1001, 40001])
+@pytest.mark.parametrize("t,alpha", [("f32", 1.25), ("f32", 2.0), ("bf16", 1.25), ("bf16", 3.0),
+                                     ("f16", 7e33)])
+def test_logits_that_alpha_takes_beyond_binary32(cs, handle, t, alpha, vocab, times):  # noqa: F811
+    """They count as infinite ones: below, masked; above, the row is NaN."""
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy(rng.standard_normal((10, vocab)) * 2).to(DT[t]).cuda()
+    low, high = float(torch.finfo(DT[t]).min), float(torch.finfo(DT[t]).max)
+    last = vocab - 1
+    x[0] = low                                         # masked throughout
+    x[1] = high
+    x[2] = low
+    x[2, vocab // 2] = 0.5                             # one left
+    x[3, vocab // 3] = high
+    x[4, last] = low                                   # the target is masked
+    x[5] = low
+    x[5, 1] = float("nan")
+    x[6] = -INF
+    x[6, 2] = low
+    x[7] = low                                         # the largest is just within the range
+    x[7, 4] = -0.9 * LARGEST / alpha
+    x[8] = 0.9 * LARGEST / alpha
+    targets = np.full(10, last, np.int32)
+    if times > 1:
+        x, targets = x.repeat(times, 1), np.tile(targets, times)
+    for k in (0, 5):
+        _check(cs, handle, x, targets, alpha, k)
+    targets[:] = -1
+    _check(cs, handle, x, targets, alpha, 0)
+
+
+@pytest.mark.parametrize("rows", [7, 700])
+def test_the_largest_alpha(cs, handle, rows):  # noqa: F811
+    """alpha times log2(e) is beyond binary32 too: only logits near zero are within it."""
+    x = torch.full((rows, 50), -1.0, device="cuda")
+    x[0, [3, 9]] = 0.0                                 # z = 0 twice
+    x[1, 5] = 1e-38                                    # z = 3, and 0 beside it
+    x[1, 7] = 0.0
+    x[3, 8] = 1.0                                      # beyond the range
+    x[4, 2] = -0.5
+    x[5, 30:] = 0.0
+    _check(cs, handle, x, np.full(rows, 7, np.int32), 3e38, 4)
