@@ -1,10 +1,16 @@
 // Layer norm y = (x - mean) * rstd * weight + bias over the rows of a matrix,
 // and its gradients with respect to x, weight and bias.
 //
-// Mean and deviations are binary32 sums.  The deviations are taken from a mean
-// (the warp's, then corrected to the row's: for parts of n_w elements with means m_w,
-// sum (x - m)^2 = sum_w [sum (x - m_w)^2 + n_w (m_w - m)^2], all terms positive), so no
-// digits are lost to a mean far from zero.
+// Mean and deviations are binary32 sums.  A warp sums the differences d of its n_w elements to a
+// number b, and their squares, in one pass.  b is an element of its own; where their mean turns
+// out to be over 4 of their deviations from it, so that the squares would lose digits, they
+// are taken again from b + sum d / n_w.  With q an element of the row, e_w = b - q + sum d / n_w
+// and e = sum n_w e_w / n,
+//   mean = q + e
+//   sum (x - mean)^2 = sum_w [sum d^2 - (sum d)^2 / n_w + n_w (e_w - e)^2]
+// so no digits are lost to a mean far from zero, and a row that hardly varies has the mean that
+// it would have near zero, rounded once.  (A mean summed from the elements as they are gave
+// a row of 7 times 1000 deviations of 6e-5, and y = -0.02 instead of 0.)
 //
 // The kernels read rows in aligned accesses wherever a row starts:
 // accesses are counted from the 16-byte boundary at or before the row's start, and
@@ -198,13 +204,24 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
         param_at[i] = e % W * pitch + e / W - 1 + tid;
     }
     const float per_dim = 1.0f / (float)dim;
+    // the warp's elements of a row
+    float count = (float)(l.lanes * W * K);
+    if constexpr (FIT != Fit::ALL) {
+        int own = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = tid * W - lead + k * step;
+            if (c < dim) own += EDGES ? min(c + W, dim) - max(c, 0) : W;
+        }
+        count = lanes_sum((float)own, l.lanes);
+    }
+    const float per_count = count > 0.0f ? __fdividef(1.0f, count) : 0.0f;
     int turn = 0;
     for (; first < p.rows; first += stride, r += stride) {
         const T* row = x.row(r);
         const int c0 = tid * W - lead;
         const bool live = FIT == Fit::ALL || r < p.rows;
         Vec<T, W> held[K];
-        int own = 0;                             // elements of the row in this lane
         auto in = [&](int k) { return FIT == Fit::ALL || (live && c0 + k * step < dim); };
         if (EDGES && x.at_ends(r, p.rows)) {
 #pragma unroll
@@ -227,69 +244,107 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < Vec<T, W>::WORDS; ++i) held[k].w[i] = in(k) ? held[k].w[i] : 0;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (in(k)) own += EDGES ? min(c0 + k * step + W, dim) - max(c0 + k * step, 0) : W;
-        uint64_t sums = pair(0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (EDGES && !in(k)) continue;
+        // b and q, 0 where they are infinite or NaN
+        auto finite = [](float v) { return fabsf(v) < INFINITY ? v : 0.0f; };
+        float base, pivot;
+        if constexpr (EDGES) {
+            base = pivot = finite(to_f32((live ? row : x.base)[0]));
+        } else {
             float f[W];
-            unpack(held[k], f);
-            if (EDGES) clear_outside(c0 + k * step, dim, f);
-#pragma unroll
-            for (int i = 0; i < W; i += 2) sums = add2(sums, pair(f[i], f[i + 1]));
+            unpack(held[0], f);
+            base = pivot = finite(__shfl_sync(ALL, f[0], lane & ~(l.lanes - 1)));
+            if (l.warps > 1) pivot = finite(to_f32(row[0]));
         }
-        float lo, hi;
-        halves(sums, lo, hi);
-        float sum = lanes_sum(lo + hi, l.lanes);
-        // any number near the mean of the warp's part will do
-        const float count = FIT == Fit::ALL ? (float)(l.lanes * W * K)
-                                            : lanes_sum((float)own, l.lanes);
-        float mean = count > 0.0f ? __fdividef(sum, count) : 0.0f;
-        sums = pair(0.0f, 0.0f);
-        uint64_t m2 = pair(-mean, -mean);
+        uint64_t d1 = pair(0.0f, 0.0f), d2 = d1;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (EDGES && !in(k)) continue;
             float f[W];
             unpack(held[k], f);
-            const float from = in(k) ? mean : 0.0f;
+            const float from = FIT == Fit::ALL || in(k) ? base : 0.0f;
             if (EDGES) {
 #pragma unroll
-                for (int i = 0; i < W; ++i) f[i] -= mean;
+                for (int i = 0; i < W; ++i) f[i] -= base;
                 clear_outside(c0 + k * step, dim, f);
             }
-            const uint64_t k2 = FIT == Fit::ALL ? m2 : pair(-from, -from);
+            const uint64_t k2 = pair(-from, -from);
 #pragma unroll
             for (int i = 0; i < W; i += 2) {
                 uint64_t d = pair(f[i], f[i + 1]);
                 if (!EDGES) d = add2(d, k2);
-                sums = fma2(d, d, sums);
+                d1 = add2(d1, d);
+                d2 = fma2(d, d, d2);
             }
         }
-        halves(sums, lo, hi);
-        float squares = lanes_sum(lo + hi, l.lanes);
+        float deviations, squares, lo, hi;
+        halves(d1, lo, hi);
+        deviations = lo + hi;
+        halves(d2, lo, hi);
+        squares = lo + hi;
+        lanes_sum(deviations, squares, l.lanes);
+        const bool far = deviations * deviations * per_count > 0.94f * squares;
+        if (__any_sync(ALL, far)) {
+            // From memory again (y, which may be x, is written behind the exchange below, or by
+            // these lanes): a second use of `held` here would cost every row registers.
+            const float better = fmaf(deviations, per_count, base);
+            float again = 0.0f, squares_again = 0.0f;
+#pragma unroll 1
+            for (int k = 0; k < K; ++k) {
+                const int c = c0 + k * step;
+                if (!in(k)) continue;
+                auto add = [&](float v) {
+                    again += v - better;
+                    squares_again = fmaf(v - better, v - better, squares_again);
+                };
+                if constexpr (EDGES) {
+#pragma unroll 1
+                    for (int e = max(c, 0); e < min(c + W, dim); ++e) add(to_f32(row[e]));
+                } else {
+                    float f[W];
+                    unpack(load_vec<Cache::KEEP, T, W>(row + c), f);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) add(f[i]);
+                }
+            }
+            lanes_sum(again, squares_again, l.lanes);
+            if (far) {
+                base = better;
+                deviations = again;
+                squares = squares_again;
+            }
+        }
+        float off = deviations * per_count;
+        squares = fmaf(-deviations, off, squares);
+        squares = squares < 0.0f ? 0.0f : squares;   // NaN stays
+        off += base - pivot;
         if (l.warps > 1) {
             // two sets of slots in turn: one barrier per row keeps them apart
             float4* s = slots[turn] + in_block * l.warps;
             turn ^= 1;
-            if (lane == 0) s[tid >> 5] = make_float4(sum, mean, squares, count);
+            if (lane == 0) s[tid >> 5] = make_float4(off * count, off, squares, count);
             row_barrier(in_block, threads);
-            sum = 0.0f;
-#pragma unroll 8
-            for (int i = 0; i < l.warps; ++i) sum += s[i].x;
-            mean = sum * per_dim;
-            squares = 0.0f;
-#pragma unroll 8
-            for (int i = 0; i < l.warps; ++i)
-                squares += s[i].z + s[i].w * (s[i].y - mean) * (s[i].y - mean);
+            if (l.warps >= 8) {
+                // a lane for each warp's part: 10 shuffles instead of 7 instructions for each
+                const float4 v = lane < l.warps ? s[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                off = warp_sum(v.x) * per_dim;
+                squares = warp_sum(fmaf(v.w * (v.y - off), v.y - off, v.z));
+            } else {
+                off = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < l.warps) off += s[i].x;
+                off *= per_dim;
+                squares = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < l.warps) squares += s[i].z + s[i].w * (s[i].y - off) * (s[i].y - off);
+            }
         }
         if (!live) continue;                     // narrow rows: a warp holds several
+        const float mean = pivot + off;
         const float rstd = rsqrtf(squares * per_dim + p.eps);
         T* y = static_cast<T*>(p.y) + r * p.ldy;
-        const uint64_t r2 = pair(rstd, rstd);
-        m2 = pair(-mean, -mean);
+        const uint64_t r2 = pair(rstd, rstd), m2 = pair(-mean, -mean);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = c0 + k * step;
@@ -354,13 +409,24 @@ __global__ __launch_bounds__(ANY_THREADS) void norm_any(NormParams p) {
         T* y = static_cast<T*>(p.y) + r * p.ldy;
         float sum = 0.0f;
         for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) sum += to_f32(x[c]);
-        const float mean = block_sum(sum, s) / (float)p.dim;
-        sum = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) {
-            const float d = to_f32(x[c]) - mean;
-            sum += d * d;
+        float mean = block_sum(sum, s) / (float)p.dim;
+        auto variance = [&] {
+            float squares = 0.0f;
+            for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) {
+                const float d = to_f32(x[c]) - mean;
+                squares += d * d;
+            }
+            return block_sum(squares, s) / (float)p.dim;
+        };
+        float var = variance();
+        if (var <= mean * mean * 0x1p-10f && mean != 0.0f) {
+            // a row that hardly varies would show the mean's rounding: the mean of the
+            // deviations corrects it
+            sum = 0.0f;
+            for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS) sum += to_f32(x[c]) - mean;
+            mean += block_sum(sum, s) / (float)p.dim;
+            var = variance();
         }
-        const float var = block_sum(sum, s) / (float)p.dim;
         const float rstd = rsqrtf(var + p.eps);
         for (int64_t c = threadIdx.x; c < p.dim; c += ANY_THREADS)
             y[c] = from_f32<T>((to_f32(x[c]) - mean) * rstd * param<P>(p.weight, c, 1.0f) +

@@ -95,3 +95,58 @@ def test_the_largest_alpha(cs, handle, rows):  # noqa: F811
     x[4, 2] = -0.5
     x[5, 30:] = 0.0
     _check(cs, handle, x, np.full(rows, 7, np.int32), 3e38, 4)
+
+
+@pytest.mark.parametrize("rows", [6, 900])
+@pytest.mark.parametrize("dim", [1, 3, 7, 100, 515, 768, 1000, 2500, 4096, 5000, 8200, 16384,
+                                 20001, 40960])
+@pytest.mark.parametrize("t", TYPES)
+def test_layer_norm_of_constant_rows(cs, handle, t, dim, rows):  # noqa: F811
+    """A constant row's mean is the constant, so its deviations are 0: y is the bias, rstd is
+    1 / sqrt(eps), and eps == 0 gives 0 * inf."""
+    if rows > 100 and dim > 9000:
+        rows = 310
+    values = torch.tensor([1000.0, 0.1, -3.3, 60001.7, 1.0 / 3.0, -0.0077], device="cuda")
+    c = values.repeat(-(-rows // 6))[:rows].to(DT[t])
+    x = c[:, None].expand(rows, dim).contiguous()
+    w = torch.linspace(0.5, 2.0, dim, device="cuda").to(DT[t])
+    b = torch.linspace(-1.0, 1.0, dim, device="cuda").to(DT[t])
+    layouts = [x]
+    if dim < 9000:
+        off = torch.empty(rows * dim + 1, dtype=DT[t], device="cuda")[1:].view(rows, dim)
+        layouts.append(off.copy_(x))                   # rows between 16-byte boundaries
+    for rows_of in layouts:
+        y, mean, rstd = cs.layer_norm(handle, rows_of, w, b, eps=1e-5)
+        assert torch.equal(mean, c.float())
+        assert torch.equal(y, b.expand(rows, dim))
+        want = 1.0 / np.sqrt(float(np.float32(1e-5)))
+        assert bool(((rstd.double() - want).abs() <= 6 * ref.U * want).all())
+        y, _, rstd = cs.layer_norm(handle, rows_of, eps=0.0)
+        assert bool(y.isnan().all()) and bool(rstd.isinf().all())
+
+
+@pytest.mark.parametrize("rows", [5, 700])
+@pytest.mark.parametrize("dim", [64, 1001, 4096, 16384, 20001])
+def test_layer_norm_of_rows_that_hardly_vary(cs, handle, dim, rows):  # noqa: F811
+    """Binary32 rows whose deviations are a few units of their last place: all that the mean's
+    own rounding (half a unit) leaves is held to, far below the sums' roundings."""
+    if rows > 100 and dim > 9000:
+        rows = 310
+    rng = np.random.default_rng(dim)
+    ulp = 2.0 ** -14                                   # of numbers in [512, 1024)
+    h_x = 700.0 + ulp * rng.integers(-20, 21, (rows, dim))
+    x = torch.from_numpy(h_x).float().cuda()
+    assert np.array_equal(_np(x), h_x)
+    y, mean, rstd = cs.layer_norm(handle, x, eps=0.0)
+    m = h_x.mean(1, keepdims=True)
+    dev = h_x - m
+    r = 1.0 / np.sqrt((dev * dev).mean(1, keepdims=True))
+    # the mean is off by half a unit for its rounding; what corrects it is a sum of deviations
+    # of at most 200 units (the first mean's error and 20), off by its chain of about 180 U of
+    # that: under 1/64 of a unit
+    d_mean = ulp * (0.5 + 1 / 64)
+    _near(_np(mean), m[:, 0], d_mean, "mean")
+    d_rstd = r * (0.5 * d_mean ** 2 * r ** 2 + ref.U * (ref.chain(dim) + 12))
+    _near(_np(rstd), r[:, 0], d_rstd[:, 0], "rstd")
+    _near(_np(y), dev * r, d_mean * (r + d_rstd) + np.abs(dev) * d_rstd + 4 * ref.U * np.abs(dev * r),
+          "y")
