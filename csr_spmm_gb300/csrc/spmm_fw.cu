@@ -314,8 +314,9 @@ __host__ __device__ inline FwTcGeo fwtc_geo(int k) {
     return g;
 }
 
+constexpr size_t FWTC_SMEM_MAX = 200 * 1024;
 inline bool fw_tc_ok(int k) {
-    return SPMM_FW_TC && k >= 1 && k <= FWTC_MAXK && fwtc_geo(k).smem <= 200 * 1024;
+    return SPMM_FW_TC && k >= 1 && k <= FWTC_MAXK && fwtc_geo(k).smem <= FWTC_SMEM_MAX;
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -767,8 +768,7 @@ cudaError_t launch_fw(const FwParams<T>& p, int grid, cudaStream_t st) {
     if constexpr (sizeof(T) == 4) {
         if (fw_tc_ok(p.k)) {
             const FwTcGeo g = fwtc_geo(p.k);
-            e = cudaFuncSetAttribute(fw_scan_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)g.smem);
+            e = allow_shared(fw_scan_tc, FWTC_SMEM_MAX);
             if (e != cudaSuccess) return e;
             fw_scan_tc<<<grid, FWTC_THREADS, g.smem, st>>>(p);
             fw_reduce<T><<<(p.k + 7) / 8 + 1, 256, 0, st>>>(p);
@@ -776,8 +776,7 @@ cudaError_t launch_fw(const FwParams<T>& p, int grid, cudaStream_t st) {
         }
     }
     if (smem > 0) {
-        e = cudaFuncSetAttribute(fw_scan<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem);
+        e = allow_shared(fw_scan<T, true>, FW_SMEM_MAX);
         if (e != cudaSuccess) return e;
         fw_scan<T, true><<<grid, FW_THREADS, smem, st>>>(p);
     } else {
@@ -794,8 +793,7 @@ int fw_blocks_per_sm(int k) {
     const size_t smem = fw_smem_bytes<T>(k);
     cudaError_t e;
     if (smem > 0) {
-        e = cudaFuncSetAttribute(fw_scan<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem);
+        e = allow_shared(fw_scan<T, true>, FW_SMEM_MAX);
         if (e == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fw_scan<T, true>, FW_THREADS,
                                                               smem);

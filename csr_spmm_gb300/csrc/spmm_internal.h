@@ -243,6 +243,14 @@ __device__ __forceinline__ void allow_successor() {
 #endif
 }
 
+// Lets `kernel` have up to `most` bytes of dynamic shared memory.  The limit is the kernel's, not
+// the caller's: `most` must be the same in every call, or one host thread would lower the limit
+// between another's call and its launch.
+template <typename... KArgs>
+inline cudaError_t allow_shared(void (*kernel)(KArgs...), size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 // Launch `kernel` on `st`, overlapping its launch with the previous kernel
 // of the stream when `overlap` is set, with an L2 access-policy window on
 // this launch alone when `win` is given (the stream's attributes are left

@@ -11,8 +11,7 @@ cudaError_t launch_long<float>(const SpmmParams<float>& p, const Geometry& g, cu
         const size_t smem = (size_t)LONG_WARPS * G * R * W * sizeof(float);
         auto kern = long_kernel<float, W, G, R>;
         if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem);
+            const cudaError_t e = allow_shared(kern, smem);     // the same for each geometry
             if (e != cudaSuccess) return e;
         }
         return launch_windowed(kern, dim3(p.long_grid), dim3(LONG_THREADS), smem, st, overlap, win, p);

@@ -840,11 +840,15 @@ int64_t blocks_of(int64_t total, int rows, int64_t most, int W) {
     return rows % W == 0 ? most : std::max<int64_t>(W, most / W * W);
 }
 
-template <typename... KArgs>
-cudaError_t allow_shared(void (*kernel)(KArgs...), size_t bytes) {
-    return bytes <= 32768 ? cudaSuccess
-                          : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)bytes);
+// Dynamic shared memory that needs no leave, and the most that a launch here asks for: the
+// parameters of the widest row with edges, and the ring of the most threads with its masks.
+constexpr size_t SHARED_FREE = 32768;
+constexpr int EDGES_COLUMNS = 16384;
+template <int W>
+constexpr size_t NORM_SHARED = (size_t)W * (EDGES_COLUMNS / W + 3) * sizeof(float2);
+template <typename T>
+constexpr size_t ring_size(int threads, int K) {
+    return ((size_t)GRAD_STAGES<T> * 2 + 1) * K * threads * 16;
 }
 
 template <typename T, typename P, int W, int K, bool WHOLE>
@@ -862,8 +866,10 @@ cudaError_t norm_launch(const NormParams& p, int64_t columns, int num_sms, cudaS
         kernel = norm_rows<T, P, W, K, Fit::ALL>;
     }
     const size_t shared = (size_t)W * pitch * sizeof(float2);
-    cudaError_t e = allow_shared(kernel, shared);
-    if (e != cudaSuccess) return e;
+    if (shared > SHARED_FREE) {
+        const cudaError_t e = allow_shared(kernel, NORM_SHARED<W>);
+        if (e != cudaSuccess) return e;
+    }
     kernel<<<(unsigned)blocks, threads, shared, st>>>(p, l, blocks * l.rows, pitch);
     return cudaGetLastError();
 }
@@ -885,14 +891,16 @@ cudaError_t norm_grad_launch(const NormGradParams& p, int64_t columns, int num_s
     const int threads = l.threads() * l.rows;
     const unsigned tiles = GIVEN ? (unsigned)((columns + GRAD_COLUMNS - 1) / GRAD_COLUMNS) : 1;
     // the ring, and masks for rows with edges
-    const size_t shared = ((size_t)GRAD_STAGES<T> * 2 + 1) * K * threads * 16;
+    const size_t shared = ring_size<T>(threads, K);
     auto kernel = norm_grad_rows<T, P, W, K, Fit::EDGES, GIVEN>;
     if (whole && l.lanes == 32 && p.dim == (int64_t)tiles * l.threads() * W * K)
         kernel = norm_grad_rows<T, P, W, K, Fit::ALL, GIVEN>;
     else if (whole)
         kernel = norm_grad_rows<T, P, W, K, Fit::WHOLE, GIVEN>;
-    cudaError_t e = allow_shared(kernel, shared);
-    if (e != cudaSuccess) return e;
+    if (shared > SHARED_FREE) {
+        const cudaError_t e = allow_shared(kernel, ring_size<T>(GRAD_THREADS, K));
+        if (e != cudaSuccess) return e;
+    }
     kernel<<<dim3((unsigned)blocks, tiles), threads, shared, st>>>(p, l, slices);
     return cudaGetLastError();
 }
@@ -932,7 +940,7 @@ cudaError_t launch_layer_norm(spmm_type_t type, spmm_type_t param_type, const No
                 if (few && columns <= 1024 * W)
                     return norm_launch<T, P, W, 1, false>(p, columns, num_sms, st);
                 // the parameters take 8 bytes of shared memory per column
-                if (columns <= 16384) return norm_launch<T, P, W, 4, false>(p, columns, num_sms, st);
+                if (columns <= EDGES_COLUMNS) return norm_launch<T, P, W, 4, false>(p, columns, num_sms, st);
             }
         }
         const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
