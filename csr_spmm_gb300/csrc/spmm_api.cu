@@ -189,8 +189,8 @@ int long_grid_of(const spmm_handle_s* h) { return long_grid_for(h->num_sms); }
 spmm_status_t grow(void** buf, size_t* have, size_t bytes) {
     if (bytes <= *have) return SPMM_OK;
     if (*buf) {
-        cudaDeviceSynchronize();     // earlier calls may still use the old buffer
-        cudaFree(*buf);
+        own_error(cudaDeviceSynchronize());     // earlier calls may still use the old buffer
+        own_error(cudaFree(*buf));
         *buf = nullptr;
         *have = 0;
     }
@@ -260,7 +260,7 @@ spmm_status_t small_product(spmm_handle_s* h, const Plan& P, const SpmmParams<T>
 
 // Records event i of the profiled call (no-op when profiling is off).
 inline void mark(spmm_handle_s* h, int i, cudaStream_t st) {
-    if (h->profiling) cudaEventRecord(h->ev[i], st);
+    if (h->profiling) own_error(cudaEventRecord(h->ev[i], st));
 }
 
 template <typename T>
@@ -307,11 +307,7 @@ spmm_status_t spmm_csr_impl(spmm_handle_t h, T alpha, const int32_t* row_ptr,
     if (!C) return SPMM_ERR_NULL_POINTER;
     const bool uses_a = alpha != T(0) && k > 0;
     if (uses_a && (!row_ptr || !col_idx || !values || !B)) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 
     if (!uses_a) {
@@ -431,11 +427,7 @@ spmm_status_t spmm_plan_impl(spmm_plan_t pl, T alpha, const int32_t* row_ptr,
     if (!C) return SPMM_ERR_NULL_POINTER;
     const bool uses_a = alpha != T(0) && k > 0;
     if (uses_a && (!row_ptr || !col_idx || !values || !B)) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!uses_a) {
         if (h->profiling) {
@@ -575,11 +567,7 @@ spmm_status_t spmm_squared_impl(spmm_handle_t h, T alpha, const int32_t* row_ptr
     if (!C) return SPMM_ERR_NULL_POINTER;
     const bool uses_a = alpha != T(0);
     if (uses_a && (!row_ptr || !col_idx || !values || !B)) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!uses_a) {
         if (h->profiling) {
@@ -671,11 +659,7 @@ spmm_status_t spmm_plan_squared_impl(spmm_plan_t pl, T alpha, const int32_t* row
     if (!C) return SPMM_ERR_NULL_POINTER;
     const bool uses_a = alpha != T(0);
     if (uses_a && (!row_ptr || !col_idx || !values || !B)) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!uses_a) {
         if (h->profiling) {
@@ -748,11 +732,7 @@ spmm_status_t spmm_fw_impl(spmm_handle_t h, int64_t n, int64_t k, const int32_t*
     if (n > 0 && (!k2b_rp || !k2b_ci || !k2b_v || !t2_rp || !t2_ci || !t2_v || !b_rp || !b_ci ||
                   !b_v))
         return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int64_t ldk = std::max<int64_t>(TILE, (k + TILE - 1) / TILE * TILE);
     const int grid = fw_blocks_per_sm<T>((int)k) * h->num_sms;
@@ -794,11 +774,7 @@ spmm_status_t spmm_ilu0_impl(spmm_handle_t h, int64_t n, int64_t nnz, const int3
     if (!h || n <= 0 || n > (int64_t)INT_MAX - 2 || nnz < 0 || nnz > (int64_t)INT_MAX)
         return SPMM_ERR_INVALID_ARGUMENT;
     if (!row_ptr || !col_idx || !values || !status) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // int words: pending[n], cnt[n], head, tail, abort, finished | dep_ptr[n+1] | queue[n] |
     // dep_idx[nnz] | piv[nnz] (int2, 8-byte aligned) | rec[16 n] (int4, 16-byte aligned) |
@@ -877,11 +853,7 @@ spmm_status_t plan_order_rows(spmm_plan_t pl, const int32_t* row_ptr, const int3
                               void* stream, bool automatic, int32_t* applied) {
     if (applied) *applied = 0;
     if (!pl) return SPMM_ERR_INVALID_ARGUMENT;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != pl->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(pl->device)) return SPMM_ERR_INVALID_ARGUMENT;
     const int n_short = pl->hdr_host[HDR_COUNT_SHORT];
     const int n_med = pl->hdr_host[HDR_COUNT_MEDIUM];
     const int64_t m = pl->m;
@@ -946,11 +918,7 @@ spmm_status_t plan_order_rows(spmm_plan_t pl, const int32_t* row_ptr, const int3
 namespace spmm {
 
 spmm_status_t lm_device(spmm_handle_t h, int* num_sms) {
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     *num_sms = h->num_sms;
     return SPMM_OK;
 }
@@ -990,12 +958,13 @@ spmm_status_t spmm_create(spmm_handle_t* out, int device) {
     h->num_sms = sms;
     h->l2_bytes = l2;
     int pmax = 0, wmax = 0;
-    if (cudaDeviceGetAttribute(&pmax, cudaDevAttrMaxPersistingL2CacheSize, device) == cudaSuccess &&
-        cudaDeviceGetAttribute(&wmax, cudaDevAttrMaxAccessPolicyWindowSize, device) == cudaSuccess) {
+    if (own_error(cudaDeviceGetAttribute(&pmax, cudaDevAttrMaxPersistingL2CacheSize, device)) ==
+            cudaSuccess &&
+        own_error(cudaDeviceGetAttribute(&wmax, cudaDevAttrMaxAccessPolicyWindowSize, device)) ==
+            cudaSuccess) {
         h->persist_max = pmax;
         h->window_max = wmax;
     }
-    cudaGetLastError();
     *out = h;
     return SPMM_OK;
 }
@@ -1003,31 +972,26 @@ spmm_status_t spmm_create(spmm_handle_t* out, int device) {
 spmm_status_t spmm_destroy(spmm_handle_t h) {
     if (!h) return SPMM_OK;
     int cur = -1;
-    cudaGetDevice(&cur);
-    if (cur != h->device) cudaSetDevice(h->device);
-    cudaDeviceSynchronize();
+    own_error(cudaGetDevice(&cur));
+    if (cur != h->device) own_error(cudaSetDevice(h->device));
+    own_error(cudaDeviceSynchronize());
     for (auto& e : h->ev)
-        if (e) cudaEventDestroy(e);
-    if (h->scratch) cudaFree(h->scratch);
-    if (h->lm_scratch) cudaFree(h->lm_scratch);
-    if (h->check_status) cudaFree(h->check_status);
+        if (e) own_error(cudaEventDestroy(e));
+    if (h->scratch) own_error(cudaFree(h->scratch));
+    if (h->lm_scratch) own_error(cudaFree(h->lm_scratch));
+    if (h->check_status) own_error(cudaFree(h->check_status));
     if (h->persist_bytes > 0) {
-        cudaCtxResetPersistingL2Cache();
-        cudaDeviceSetLimit(cudaLimitPersistingL2CacheSize, h->persist_prev);
+        own_error(cudaCtxResetPersistingL2Cache());
+        own_error(cudaDeviceSetLimit(cudaLimitPersistingL2CacheSize, h->persist_prev));
     }
-    if (cur >= 0 && cur != h->device) cudaSetDevice(cur);
-    cudaGetLastError();
+    if (cur >= 0 && cur != h->device) own_error(cudaSetDevice(cur));
     delete h;
     return SPMM_OK;
 }
 
 spmm_status_t spmm_reserve(spmm_handle_t h, int64_t m, int64_t n, int elem_size) {
     if (!h || m < 0 || n < 0 || (elem_size != 4 && elem_size != 8)) return SPMM_ERR_INVALID_ARGUMENT;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     return ensure_scratch(h, layout_for(m, n, elem_size, long_grid_of(h)).total);
 }
 
@@ -1053,11 +1017,7 @@ spmm_status_t spmm_csr_check(spmm_handle_t h, const int32_t* row_ptr, const int3
     if (!h || !host_status) return !h ? SPMM_ERR_INVALID_ARGUMENT : SPMM_ERR_NULL_POINTER;
     if (m < 0 || k < 0 || nnz < 0) return SPMM_ERR_INVALID_ARGUMENT;
     if (!row_ptr || (nnz > 0 && !col_idx)) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!h->check_status && cudaMalloc(&h->check_status, sizeof(int)) != cudaSuccess) {
         cudaGetLastError();
@@ -1080,11 +1040,7 @@ spmm_status_t spmm_csr_check(spmm_handle_t h, const int32_t* row_ptr, const int3
 spmm_status_t spmm_measure_fp64_fma_rate(spmm_handle_t h, double* fma_per_second) {
     if (!h) return SPMM_ERR_INVALID_ARGUMENT;
     if (!fma_per_second) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     // 32 warps per SM, 8 independent chains per thread: enough FMAs in flight
     // to cover the pipe's latency
     const int grid = 4 * h->num_sms;
@@ -1123,11 +1079,7 @@ spmm_status_t spmm_measure_fp64_fma_rate(spmm_handle_t h, double* fma_per_second
 spmm_status_t spmm_set_profiling(spmm_handle_t h, int enable) {
     if (!h) return SPMM_ERR_INVALID_ARGUMENT;
     if (enable && !h->ev[0]) {
-        int cur = -1;
-        if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-            cudaGetLastError();
-            return SPMM_ERR_INVALID_ARGUMENT;
-        }
+        if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
         for (auto& e : h->ev) {
             if (cudaEventCreate(&e) != cudaSuccess) {
                 cudaGetLastError();
@@ -1182,11 +1134,7 @@ spmm_status_t spmm_plan_create(spmm_handle_t h, spmm_plan_t* out, const int32_t*
     if (m > (int64_t)INT_MAX - BIN_TILE || k > (int64_t)INT_MAX || n > (int64_t)INT_MAX)
         return SPMM_ERR_INVALID_ARGUMENT;
     if (m > 0 && !row_ptr) return SPMM_ERR_NULL_POINTER;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     spmm_plan_s* pl = new (std::nothrow) spmm_plan_s();
     if (!pl) return SPMM_ERR_ALLOC;
     pl->h = h;
@@ -1236,12 +1184,11 @@ spmm_status_t spmm_plan_create(spmm_handle_t h, spmm_plan_t* out, const int32_t*
 spmm_status_t spmm_plan_destroy(spmm_plan_t pl) {
     if (!pl) return SPMM_OK;
     int cur = -1;
-    cudaGetDevice(&cur);
-    if (cur != pl->device) cudaSetDevice(pl->device);
-    cudaDeviceSynchronize();
-    cudaFree(pl->scratch);
-    if (cur >= 0 && cur != pl->device) cudaSetDevice(cur);
-    cudaGetLastError();
+    own_error(cudaGetDevice(&cur));
+    if (cur != pl->device) own_error(cudaSetDevice(pl->device));
+    own_error(cudaDeviceSynchronize());
+    own_error(cudaFree(pl->scratch));
+    if (cur >= 0 && cur != pl->device) own_error(cudaSetDevice(cur));
     delete pl;
     return SPMM_OK;
 }
@@ -1281,11 +1228,7 @@ spmm_status_t spmm_plan_csr_f64(spmm_plan_t plan, double alpha, const int32_t* r
 
 spmm_status_t spmm_set_l2_persistence(spmm_handle_t h, int64_t bytes) {
     if (!h) return SPMM_ERR_INVALID_ARGUMENT;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) {
-        cudaGetLastError();
-        return SPMM_ERR_INVALID_ARGUMENT;
-    }
+    if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
     if (bytes == 0) {
         if (h->persist_bytes > 0) {
             cudaError_t e1 = cudaCtxResetPersistingL2Cache();

@@ -191,8 +191,7 @@ cudaError_t launch_embed(const EmbedParams& p, bool whole, int num_sms, cudaStre
         int64_t rows = std::max<int64_t>(1, EMBED_THREADS * 8 / nv);
         rows = std::max<int64_t>(1, std::min<int64_t>(rows, p.tokens / (4 * num_sms)));
         const unsigned blocks = (unsigned)((p.tokens + rows - 1) / rows);
-        embed_rows<T><<<blocks, EMBED_THREADS, 0, st>>>(p, nv, (int)rows);
-        return cudaGetLastError();
+        return launch(embed_rows<T>, blocks, EMBED_THREADS, 0, st, p, nv, (int)rows);
     }
     // a row between boundaries covers up to W - 1 elements more
     const int64_t nv = (p.dim + 2 * (W - 1)) / W;
@@ -207,8 +206,7 @@ cudaError_t launch_embed(const EmbedParams& p, bool whole, int num_sms, cudaStre
     const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(
                                           parts, std::max<int64_t>(1, 4 * num_sms / blocks)));
     auto run = [&](auto kernel) {
-        kernel<<<grid, EMBED_THREADS, 0, st>>>(p, lanes_log, parts, used);
-        return cudaGetLastError();
+        return launch(kernel, grid, EMBED_THREADS, 0, st, p, lanes_log, parts, used);
     };
     return rows == 4   ? run(embed_shifted<T, 4>)
            : rows == 2 ? run(embed_shifted<T, 2>) : run(embed_shifted<T, 1>);
@@ -812,9 +810,8 @@ cudaError_t launch_embedding_grad(spmm_type_t type, spmm_type_t grad_type,
         p.beta == 1.0f ? 0 : (p.vocab + k.fill_rows - 1) / k.fill_rows;
     if (p.tokens > 0) {
         const int tiles = (int)((p.tokens + SORT_TILE - 1) / SORT_TILE);
-        sort_tiles<<<tiles, SORT_TILE, 0, st>>>(p.ids, (int)p.tokens, p.vocab, keys, k.arrived,
-                                                k.sum_items * COUNTERS);
-        cudaError_t e = cudaGetLastError();
+        cudaError_t e = launch(sort_tiles, tiles, SORT_TILE, 0, st, p.ids, (int)p.tokens, p.vocab,
+                               keys, k.arrived, k.sum_items * COUNTERS);
         const unsigned total = (unsigned)tiles * SORT_TILE;
         for (int64_t run = SORT_TILE; e == cudaSuccess && run < total;) {
             const int64_t runs = (total + run - 1) / run;

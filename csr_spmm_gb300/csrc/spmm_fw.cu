@@ -761,29 +761,29 @@ size_t fw_smem_bytes(int k) {
 
 template <typename T>
 cudaError_t launch_fw(const FwParams<T>& p, int grid, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(p.t1d, 0, sizeof(T) * (size_t)p.k * p.ldk, st);
+    const int reduce = (p.k + 7) / 8 + 1;
+    cudaError_t e =
+        own_error(cudaMemsetAsync(p.t1d, 0, sizeof(T) * (size_t)p.k * p.ldk, st));
+    if (e == cudaSuccess && p.k > 0) e = launch(fw_densify<T>, (p.k + 7) / 8, 256, 0, st, p);
     if (e != cudaSuccess) return e;
-    if (p.k > 0) fw_densify<T><<<(p.k + 7) / 8, 256, 0, st>>>(p);
     const size_t smem = fw_smem_bytes<T>(p.k);
     if constexpr (sizeof(T) == 4) {
         if (fw_tc_ok(p.k)) {
             const FwTcGeo g = fwtc_geo(p.k);
             e = allow_shared(fw_scan_tc, FWTC_SMEM_MAX);
-            if (e != cudaSuccess) return e;
-            fw_scan_tc<<<grid, FWTC_THREADS, g.smem, st>>>(p);
-            fw_reduce<T><<<(p.k + 7) / 8 + 1, 256, 0, st>>>(p);
-            return cudaGetLastError();
+            if (e == cudaSuccess) e = launch(fw_scan_tc, grid, FWTC_THREADS, g.smem, st, p);
+            if (e == cudaSuccess) e = launch(fw_reduce<T>, reduce, 256, 0, st, p);
+            return e;
         }
     }
     if (smem > 0) {
         e = allow_shared(fw_scan<T, true>, FW_SMEM_MAX);
-        if (e != cudaSuccess) return e;
-        fw_scan<T, true><<<grid, FW_THREADS, smem, st>>>(p);
+        if (e == cudaSuccess) e = launch(fw_scan<T, true>, grid, FW_THREADS, smem, st, p);
     } else {
-        fw_scan<T, false><<<grid, FW_THREADS, 0, st>>>(p);
+        e = launch(fw_scan<T, false>, grid, FW_THREADS, 0, st, p);
     }
-    fw_reduce<T><<<(p.k + 7) / 8 + 1, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    if (e == cudaSuccess) e = launch(fw_reduce<T>, reduce, 256, 0, st, p);
+    return e;
 }
 
 template <typename T>

@@ -644,15 +644,16 @@ __global__ void __launch_bounds__(ILU0_THREADS, 2) ilu0_factor(Ilu0Params<T> p) 
 template <typename T>
 cudaError_t launch_ilu0(const Ilu0Params<T>& p, int grid, cudaStream_t st) {
     const int rb = (p.n + 255) / 256;
-    ilu0_count<T><<<rb, 256, 0, st>>>(p);
     const int ntiles = (int)(((int64_t)p.n + ILU0_SCAN_TILE - 1) / ILU0_SCAN_TILE);
-    ilu0_scan_tiles<T><<<ntiles, ILU0_SCAN_TILE, 0, st>>>(p);
-    ilu0_scan_sums<T><<<1, ILU0_SCAN_TILE, 0, st>>>(p, ntiles);
-    ilu0_scan_apply<T><<<ntiles, ILU0_SCAN_TILE, 0, st>>>(p);
-    ilu0_fill<T><<<rb, 256, 0, st>>>(p);
-    ilu0_records<T><<<(unsigned)(((int64_t)p.n * ILU0_REC_LANES + 255) / 256), 256, 0, st>>>(p);
-    ilu0_factor<T><<<grid, ILU0_THREADS, 0, st>>>(p);
-    return cudaGetLastError();
+    const unsigned records = (unsigned)(((int64_t)p.n * ILU0_REC_LANES + 255) / 256);
+    cudaError_t e = launch(ilu0_count<T>, rb, 256, 0, st, p);
+    if (e == cudaSuccess) e = launch(ilu0_scan_tiles<T>, ntiles, ILU0_SCAN_TILE, 0, st, p);
+    if (e == cudaSuccess) e = launch(ilu0_scan_sums<T>, 1, ILU0_SCAN_TILE, 0, st, p, ntiles);
+    if (e == cudaSuccess) e = launch(ilu0_scan_apply<T>, ntiles, ILU0_SCAN_TILE, 0, st, p);
+    if (e == cudaSuccess) e = launch(ilu0_fill<T>, rb, 256, 0, st, p);
+    if (e == cudaSuccess) e = launch(ilu0_records<T>, records, 256, 0, st, p);
+    if (e == cudaSuccess) e = launch(ilu0_factor<T>, grid, ILU0_THREADS, 0, st, p);
+    return e;
 }
 
 template <typename T>

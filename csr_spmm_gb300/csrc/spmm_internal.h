@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 namespace spmm {
@@ -243,12 +244,33 @@ __device__ __forceinline__ void allow_successor() {
 #endif
 }
 
+// The status of a runtime call of ours, with the error that it left taken back.  The runtime and
+// its last error are the process's: an error that the caller has pending is neither taken for
+// a launch's (each is judged by what it returns, never by cudaGetLastError) nor cleared by calls
+// that succeed, and none of ours is left for the caller.
+inline cudaError_t own_error(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+inline bool is_current(int device) {
+    int cur = -1;
+    return own_error(cudaGetDevice(&cur)) == cudaSuccess && cur == device;
+}
+
 // Lets `kernel` have up to `most` bytes of dynamic shared memory.  The limit is the kernel's, not
 // the caller's: `most` must be the same in every call, or one host thread would lower the limit
-// between another's call and its launch.
+// between another's call and its launch.  (cudaFuncSetAttribute would do, but it clears the
+// last error even where it succeeds.)
 template <typename... KArgs>
 inline cudaError_t allow_shared(void (*kernel)(KArgs...), size_t most) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    int device = 0;
+    cudaKernel_t k;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaGetKernel(&k, reinterpret_cast<const void*>(kernel));
+    if (e == cudaSuccess)
+        e = cudaKernelSetAttributeForDevice(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            (int)most, device);
+    return own_error(e);
 }
 
 // Launch `kernel` on `st`, overlapping its launch with the previous kernel
@@ -282,13 +304,21 @@ inline cudaError_t launch_windowed(void (*kernel)(KArgs...), dim3 grid, dim3 blo
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    return own_error(cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...));
 }
 
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                                   cudaStream_t st, bool overlap, Args... args) {
     return launch_windowed(kernel, grid, block, smem, st, overlap, nullptr, args...);
+}
+
+template <typename... KArgs>
+inline cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t st, std::type_identity_t<KArgs>... args) {
+    void* addresses[] = {&args...};
+    return own_error(cudaLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, addresses,
+                                      smem, st));
 }
 
 }  // namespace spmm

@@ -25,11 +25,7 @@ inline bool bad_pair(spmm_type_t t, spmm_type_t other) {
 inline bool bad_count(int64_t n, int64_t most) { return n < 0 || n > most; }
 inline bool short_ld(int64_t ld, int64_t cols) { return ld < std::max<int64_t>(1, cols); }
 
-inline spmm_status_t launched(cudaError_t e) {
-    if (e == cudaSuccess) return SPMM_OK;
-    cudaGetLastError();
-    return SPMM_ERR_CUDA;
-}
+inline spmm_status_t launched(cudaError_t e) { return e == cudaSuccess ? SPMM_OK : SPMM_ERR_CUDA; }
 
 }  // namespace
 

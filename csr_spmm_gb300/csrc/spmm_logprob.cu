@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cooperative_groups.h>
 
+#include "spmm_internal.h"
 #include "spmm_lm_device.cuh"
 
 namespace spmm {
@@ -644,7 +645,7 @@ cudaError_t launch_forward(const LogprobParams& p, int num_sms, cudaStream_t st)
     auto kernel = p.top_k > 0
                       ? (split > 1 ? logprob_rows<T, true, true> : logprob_rows<T, true, false>)
                       : (split > 1 ? logprob_rows<T, false, true> : logprob_rows<T, false, false>);
-    return cudaLaunchKernelEx(&cfg, kernel, p, split);
+    return own_error(cudaLaunchKernelEx(&cfg, kernel, p, split));
 }
 
 // ---- gradient ---------------------------------------------------------------------------
@@ -727,8 +728,7 @@ cudaError_t launch_grad(const LogprobGradParams& p, cudaStream_t st) {
     while (threads > 64 && nvec <= threads / 2 * LG_BATCH) threads /= 2;
     const int64_t whole = (nvec + threads * LG_BATCH - 1) / (threads * LG_BATCH);
     const int pieces = (int)std::max<int64_t>(1, std::min<int64_t>(whole, 0x7fffffff / p.rows));
-    logprob_grad_rows<T, W><<<(unsigned)(p.rows * pieces), threads, 0, st>>>(p, pieces);
-    return cudaGetLastError();
+    return launch(logprob_grad_rows<T, W>, (unsigned)(p.rows * pieces), threads, 0, st, p, pieces);
 }
 
 }  // namespace

@@ -63,15 +63,13 @@ __global__ void __launch_bounds__(256) fp64_fma_probe(double x, double y, int it
 
 cudaError_t launch_fp64_fma_probe(int grid, int iters, double* sink, cudaStream_t st,
                                   int64_t* fmas) {
-    fp64_fma_probe<<<grid, 256, 0, st>>>(0.999999999, 1e-12, iters, sink);
     *fmas = (int64_t)grid * 256 * FMA_CHAINS * iters;
-    return cudaGetLastError();
+    return launch(fp64_fma_probe, grid, 256, 0, st, 0.999999999, 1e-12, iters, sink);
 }
 
 template <typename T>
 cudaError_t launch_scale(T* C, int64_t ldc, int m, int n, T beta, int grid, cudaStream_t st) {
-    scale_kernel<T><<<grid, 256, 0, st>>>(C, ldc, m, n, beta);
-    return cudaGetLastError();
+    return launch(scale_kernel<T>, grid, 256, 0, st, C, ldc, m, n, beta);
 }
 template cudaError_t launch_scale<float>(float*, int64_t, int, int, float, int, cudaStream_t);
 template cudaError_t launch_scale<double>(double*, int64_t, int, int, double, int, cudaStream_t);
@@ -82,8 +80,7 @@ cudaError_t launch_csr_check(const int* row_ptr, const int* col_idx, int64_t m, 
     int grid = (int)((work + 255) / 256);
     if (grid < 1) grid = 1;
     if (grid > 4096) grid = 4096;
-    csr_check_kernel<<<grid, 256, 0, st>>>(row_ptr, col_idx, m, k, nnz, status);
-    return cudaGetLastError();
+    return launch(csr_check_kernel, grid, 256, 0, st, row_ptr, col_idx, m, k, nnz, status);
 }
 
 }  // namespace spmm

@@ -870,8 +870,7 @@ cudaError_t norm_launch(const NormParams& p, int64_t columns, int num_sms, cudaS
         const cudaError_t e = allow_shared(kernel, NORM_SHARED<W>);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<(unsigned)blocks, threads, shared, st>>>(p, l, blocks * l.rows, pitch);
-    return cudaGetLastError();
+    return launch(kernel, (unsigned)blocks, threads, shared, st, p, l, blocks * l.rows, pitch);
 }
 
 // Row groups (slices) of the gradient's grid at 512 threads per SM.
@@ -901,8 +900,7 @@ cudaError_t norm_grad_launch(const NormGradParams& p, int64_t columns, int num_s
         const cudaError_t e = allow_shared(kernel, ring_size<T>(GRAD_THREADS, K));
         if (e != cudaSuccess) return e;
     }
-    kernel<<<dim3((unsigned)blocks, tiles), threads, shared, st>>>(p, l, slices);
-    return cudaGetLastError();
+    return launch(kernel, dim3((unsigned)blocks, tiles), threads, shared, st, p, l, slices);
 }
 
 template <typename F>
@@ -944,8 +942,7 @@ cudaError_t launch_layer_norm(spmm_type_t type, spmm_type_t param_type, const No
             }
         }
         const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
-        norm_any<T, P><<<blocks, ANY_THREADS, 0, st>>>(p);
-        return cudaGetLastError();
+        return launch(norm_any<T, P>, blocks, ANY_THREADS, 0, st, p);
     });
 }
 
@@ -977,11 +974,9 @@ cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,
                 e = norm_grad_launch<T, P, false>(p, columns, num_sms, st, &slices);
             } else {
                 const unsigned blocks = (unsigned)std::min<int64_t>(p.rows, num_sms * 8);
-                if (alike(p.x, p.ldx, p.dy, p.ld_dy, sizeof(T)))
-                    grad_means<T, P, W><<<blocks, ANY_THREADS, 0, st>>>(p);
-                else
-                    grad_means<T, P, 1><<<blocks, ANY_THREADS, 0, st>>>(p);
-                e = cudaGetLastError();
+                auto means = alike(p.x, p.ldx, p.dy, p.ld_dy, sizeof(T)) ? grad_means<T, P, W>
+                                                                         : grad_means<T, P, 1>;
+                e = launch(means, blocks, ANY_THREADS, 0, st, p);
                 if (e != cudaSuccess) return e;
                 if (same) {
                     e = norm_grad_launch<T, P, true>(p, columns, num_sms, st, &slices);
@@ -989,8 +984,8 @@ cudaError_t launch_layer_norm_grad(spmm_type_t type, spmm_type_t param_type,
                     slices = (int)slices_any(p.rows);
                     const dim3 grid((unsigned)((p.dim + ANY_THREADS - 1) / ANY_THREADS),
                                     (unsigned)slices);
-                    norm_grad_any<T, P><<<grid, ANY_THREADS, 0, st>>>(p, slice_rows(p.rows));
-                    e = cudaGetLastError();
+                    e = launch(norm_grad_any<T, P>, grid, ANY_THREADS, 0, st, p,
+                               slice_rows(p.rows));
                 }
             }
         }

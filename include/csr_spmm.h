@@ -40,6 +40,11 @@
  * surfaces at the caller's next synchronisation.  A handle may be used by one
  * stream at a time (its scratch is shared by its calls).
  *
+ * The CUDA runtime is the process's shared one, and with it the thread's last
+ * error: a call judges its own runtime calls and launches by what they return,
+ * so an error that the caller has pending (cudaPeekAtLastError) is neither
+ * reported as the call's nor cleared by a call that succeeds.
+ *
  * CSR contents are a precondition: row_ptr[0] == 0, row_ptr non-decreasing,
  * 0 <= col_idx[p] < k.  They are not checked on the product path (nor are
  * they on the page); spmm_csr_check verifies them on the device.
