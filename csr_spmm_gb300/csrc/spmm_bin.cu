@@ -203,8 +203,8 @@ bin_count_kernel(const int* __restrict__ row_ptr, int m, int short_max, int long
 constexpr int SCAN_THREADS = 1024;
 
 __global__ void __launch_bounds__(SCAN_THREADS)
-bin_scan_kernel(const int* __restrict__ tile_counts, int tiles, int* __restrict__ tile_offsets,
-                int* __restrict__ hdr, int* __restrict__ med_pre, int* __restrict__ long_pre) {
+bin_scan_kernel(const int* tile_counts, int tiles, int* tile_offsets, int* __restrict__ hdr,
+                int* __restrict__ med_pre, int* __restrict__ long_pre) {
     __shared__ int s_warp[32][R_USED];
     __shared__ int s_carry[R_USED];
     wait_for_predecessor();
@@ -269,8 +269,8 @@ bin_scan_kernel(const int* __restrict__ tile_counts, int tiles, int* __restrict_
 template <int ITEMS, bool SELF>
 __global__ void __launch_bounds__(BIN_THREADS)
 bin_scatter_kernel(const int* __restrict__ row_ptr, int m, int short_max, int long_min,
-                   const int* __restrict__ tile_counts, const int* __restrict__ tile_offsets,
-                   int tiles, int* __restrict__ hdr, int* __restrict__ rowlist,
+                   const int* tile_counts, const int* tile_offsets, int tiles,
+                   int* __restrict__ hdr, int* __restrict__ rowlist,
                    int* __restrict__ med_pre, int* __restrict__ long_pre,
                    int* __restrict__ long_cnt) {
     constexpr int NW = BIN_THREADS / 32;

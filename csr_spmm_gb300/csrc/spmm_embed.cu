@@ -286,10 +286,11 @@ __device__ __forceinline__ int count_below(const uint64_t* a, int n, uint64_t ke
 // for neighbouring keys, so their probes share memory words, and a search is one chain
 // of loads with many others beside it: 8192 keys 5 us (one thread per key with WAYS
 // chains: 25 us, its loads waiting for one another).  Behind the `total` keys (whole
-// tiles) lies a largest one, which ends every search that would go further.
+// tiles) lies a largest one, which ends every search that would go further.  The keys are
+// read through ordinary loads: the kernel may start while its predecessor writes them, so
+// they are not constant for its lifetime.
 template <int WAYS>
-__global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restrict__ in,
-                                                        uint64_t* __restrict__ out,
+__global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* in, uint64_t* out,
                                                         unsigned total, unsigned run) {
     __shared__ unsigned count[WAYS][32];
     allow_successor();
@@ -310,8 +311,8 @@ __global__ __launch_bounds__(32 * WAYS) void merge_runs(const uint64_t* __restri
     } else {
         const unsigned bound = (unsigned)(key >> 32) + (q < own);
         for (unsigned half = run >> 1; half > 0; half >>= 1)
-            below += __ldg(ids + 2 * min(below + half - 1, total)) < bound ? half : 0;
-        below += __ldg(ids + 2 * min(below, total)) < bound;    // one candidate is left
+            below += ids[2 * min(below + half - 1, total)] < bound ? half : 0;
+        below += ids[2 * min(below, total)] < bound;            // one candidate is left
     }
     count[q][lane] = below - start;
     __syncthreads();

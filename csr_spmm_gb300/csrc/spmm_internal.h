@@ -231,7 +231,8 @@ namespace spmm {
 
 // Programmatic dependent launch: a kernel of the chain may be launched while
 // its predecessor drains; it waits here before touching the predecessor's
-// output (a no-op when launched without the attribute).
+// output (a no-op when launched without the attribute).  That output is not constant for
+// the kernel's lifetime: no const __restrict__ parameter and no __ldg reads it.
 __device__ __forceinline__ void wait_for_predecessor() {
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");
