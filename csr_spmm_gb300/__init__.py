@@ -75,7 +75,9 @@ class Handle:
         spmm_reserve(self.ptr, m, n, elem_size)
 
     def reserve_lm(self, rows: int, dim: int) -> None:
-        """Scratch of embedding_grad and layer_norm_grad for up to rows x dim inputs."""
+        """Scratch of embedding_grad and layer_norm_grad for up to rows x dim inputs, so that
+        they allocate nothing (in a stream capture they must not).  A captured graph's scratch
+        stays its own until :meth:`close`, whatever later calls need."""
         spmm_reserve_lm(self.ptr, rows, dim)
 
     def close(self) -> None:

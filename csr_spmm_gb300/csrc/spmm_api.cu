@@ -17,6 +17,13 @@
 
 using namespace spmm;
 
+// A device buffer of a handle, grown on demand.
+struct Scratch {
+    void* at = nullptr;
+    size_t bytes = 0;
+    bool captured = false;            // a CUDA graph may hold its address
+};
+
 struct spmm_handle_s {
     int device = 0;
     int num_sms = 0;
@@ -25,10 +32,9 @@ struct spmm_handle_s {
     int64_t window_max = 0;           // largest access-policy window
     int64_t persist_bytes = 0;        // set-aside this handle asked for (0: off)
     size_t persist_prev = 0;          // the limit before, restored on destroy
-    void* scratch = nullptr;
-    size_t scratch_bytes = 0;
-    void* lm_scratch = nullptr;       // the language-model operators' own (spmm_lm_api.cu)
-    size_t lm_scratch_bytes = 0;
+    Scratch scratch;
+    Scratch lm_scratch;               // the language-model operators' own (spmm_lm_api.cu)
+    std::vector<void*> kept;          // buffers of captured graphs that have since grown
     int* check_status = nullptr;
     // occupancy cache of the rows kernel, keyed by (element size, W, G, R)
     struct OccEntry { int es, W, G, R, blocks; };
@@ -185,27 +191,47 @@ ScratchLayout layout_for(int64_t m, int64_t n, int es, int long_grid) {
 
 int long_grid_of(const spmm_handle_s* h) { return long_grid_for(h->num_sms); }
 
-// Grow a device buffer of the handle to at least `bytes` (contents are lost).
-spmm_status_t grow(void** buf, size_t* have, size_t bytes) {
-    if (bytes <= *have) return SPMM_OK;
-    if (*buf) {
-        own_error(cudaDeviceSynchronize());     // earlier calls may still use the old buffer
-        own_error(cudaFree(*buf));
-        *buf = nullptr;
-        *have = 0;
+// Whether the calls on `st` go into a graph.  The legacy stream's never do (and it may not be
+// asked while another stream is captured).
+bool capturing(cudaStream_t st) {
+    if (!st || st == cudaStreamLegacy) return false;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    return own_error(cudaStreamIsCapturing(st, &status)) == cudaSuccess &&
+           status != cudaStreamCaptureStatusNone;
+}
+
+// Grow a buffer of the handle to at least `bytes` for a call on `st` (contents are lost).  A
+// graph keeps the address that its calls had: a buffer that one may hold is given back with the
+// handle only.  So is one that is outgrown within a capture, where its last use cannot be
+// waited for.
+spmm_status_t grow(spmm_handle_s* h, Scratch* s, size_t bytes, cudaStream_t st) {
+    const bool more = bytes > s->bytes;
+    const bool now = (more || !s->captured) && capturing(st);
+    if (more) {
+        if (s->at && (s->captured || now)) {
+            try {
+                h->kept.push_back(s->at);
+            } catch (const std::bad_alloc&) {          // no C++ exception crosses the C ABI
+                return SPMM_ERR_ALLOC;
+            }
+        } else if (s->at) {
+            own_error(cudaDeviceSynchronize());        // earlier calls may still use it
+            own_error(cudaFree(s->at));
+        }
+        *s = Scratch{};
+        const size_t want = align_up(bytes + bytes / 4, 1 << 20);
+        if (own_error(cudaMalloc(&s->at, want)) != cudaSuccess) {
+            s->at = nullptr;
+            return SPMM_ERR_ALLOC;
+        }
+        s->bytes = want;
     }
-    const size_t want = align_up(bytes + bytes / 4, 1 << 20);
-    if (cudaMalloc(buf, want) != cudaSuccess) {
-        cudaGetLastError();
-        *buf = nullptr;
-        return SPMM_ERR_ALLOC;
-    }
-    *have = want;
+    s->captured |= now;
     return SPMM_OK;
 }
 
-spmm_status_t ensure_scratch(spmm_handle_s* h, size_t bytes) {
-    return grow(&h->scratch, &h->scratch_bytes, bytes);
+spmm_status_t ensure_scratch(spmm_handle_s* h, size_t bytes, cudaStream_t st) {
+    return grow(h, &h->scratch, bytes, st);
 }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -345,9 +371,9 @@ spmm_status_t spmm_csr_impl(spmm_handle_t h, T alpha, const int32_t* row_ptr,
     }
     const int lg = long_grid_of(h);
     const ScratchLayout L = layout_for(m, n, (int)sizeof(T), lg);
-    spmm_status_t s = ensure_scratch(h, L.total);
+    spmm_status_t s = ensure_scratch(h, L.total, st);
     if (s != SPMM_OK) return s;
-    char* base = static_cast<char*>(h->scratch);
+    char* base = static_cast<char*>(h->scratch.at);
 
     BinScratch bs{};
     bs.hdr = reinterpret_cast<int*>(base + L.hdr);
@@ -587,9 +613,9 @@ spmm_status_t spmm_squared_impl(spmm_handle_t h, T alpha, const int32_t* row_ptr
     const int lg = long_grid_of(h);
     const ScratchLayout L = layout_for(m, n, (int)sizeof(T), lg);
     const size_t t_off = align_up(L.total, 256);
-    spmm_status_t s = ensure_scratch(h, t_off + (size_t)m * (size_t)ldt * sizeof(T));
+    spmm_status_t s = ensure_scratch(h, t_off + (size_t)m * (size_t)ldt * sizeof(T), st);
     if (s != SPMM_OK) return s;
-    char* base = static_cast<char*>(h->scratch);
+    char* base = static_cast<char*>(h->scratch.at);
     T* Tm = reinterpret_cast<T*>(base + t_off);
 
     BinScratch bs{};
@@ -675,9 +701,9 @@ spmm_status_t spmm_plan_squared_impl(spmm_plan_t pl, T alpha, const int32_t* row
     constexpr int64_t WV = 16 / (int64_t)sizeof(T);
     const int64_t ldt = (n + WV - 1) / WV * WV;
     if (ldt > (int64_t)INT_MAX) return SPMM_ERR_INVALID_ARGUMENT;
-    spmm_status_t s = ensure_scratch(h, (size_t)m * (size_t)ldt * sizeof(T));
+    spmm_status_t s = ensure_scratch(h, (size_t)m * (size_t)ldt * sizeof(T), st);
     if (s != SPMM_OK) return s;
-    T* Tm = static_cast<T*>(h->scratch);
+    T* Tm = static_cast<T*>(h->scratch.at);
 
     SpmmParams<T> p{};
     p.row_ptr = row_ptr;
@@ -742,9 +768,9 @@ spmm_status_t spmm_fw_impl(spmm_handle_t h, int64_t n, int64_t k, const int32_t*
     const size_t o_pv = off;   off = align_up(off + sizeof(T) * (size_t)grid * ldk, 256);
     const size_t o_pi = off;   off = align_up(off + sizeof(int) * (size_t)grid * ldk, 256);
     const size_t o_pg = off;   off = align_up(off + sizeof(double) * (size_t)grid, 256);
-    spmm_status_t s = ensure_scratch(h, off);
+    spmm_status_t s = ensure_scratch(h, off, st);
     if (s != SPMM_OK) return s;
-    char* base = static_cast<char*>(h->scratch);
+    char* base = static_cast<char*>(h->scratch.at);
     FwParams<T> p{};
     p.n = (int)n;
     p.k = (int)k;
@@ -788,9 +814,9 @@ spmm_status_t spmm_ilu0_impl(spmm_handle_t h, int64_t n, int64_t nnz, const int3
     const size_t o_done = o_pub + nz1 * (sizeof(T) / sizeof(int));
     const size_t o_tile = o_done + (size_t)n;
     const size_t words = o_tile + ((size_t)n + 1023) / 1024 + 1;
-    spmm_status_t s = ensure_scratch(h, words * sizeof(int));
+    spmm_status_t s = ensure_scratch(h, words * sizeof(int), st);
     if (s != SPMM_OK) return s;
-    int* w = static_cast<int*>(h->scratch);
+    int* w = static_cast<int*>(h->scratch.at);
     if (cudaMemsetAsync(w, 0, zero_words * sizeof(int), st) != cudaSuccess ||
         cudaMemsetAsync(w + o_q, 0xff, (size_t)n * sizeof(int), st) != cudaSuccess ||
         cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) {
@@ -923,9 +949,9 @@ spmm_status_t lm_device(spmm_handle_t h, int* num_sms) {
     return SPMM_OK;
 }
 
-spmm_status_t lm_scratch(spmm_handle_t h, size_t bytes, char** base) {
-    const spmm_status_t s = grow(&h->lm_scratch, &h->lm_scratch_bytes, bytes);
-    *base = static_cast<char*>(h->lm_scratch);
+spmm_status_t lm_scratch(spmm_handle_t h, size_t bytes, cudaStream_t st, char** base) {
+    const spmm_status_t s = grow(h, &h->lm_scratch, bytes, st);
+    *base = static_cast<char*>(h->lm_scratch.at);
     return s;
 }
 
@@ -977,8 +1003,9 @@ spmm_status_t spmm_destroy(spmm_handle_t h) {
     own_error(cudaDeviceSynchronize());
     for (auto& e : h->ev)
         if (e) own_error(cudaEventDestroy(e));
-    if (h->scratch) own_error(cudaFree(h->scratch));
-    if (h->lm_scratch) own_error(cudaFree(h->lm_scratch));
+    for (void* buffer : h->kept) own_error(cudaFree(buffer));
+    for (void* buffer : {h->scratch.at, h->lm_scratch.at})
+        if (buffer) own_error(cudaFree(buffer));
     if (h->check_status) own_error(cudaFree(h->check_status));
     if (h->persist_bytes > 0) {
         own_error(cudaCtxResetPersistingL2Cache());
@@ -992,7 +1019,7 @@ spmm_status_t spmm_destroy(spmm_handle_t h) {
 spmm_status_t spmm_reserve(spmm_handle_t h, int64_t m, int64_t n, int elem_size) {
     if (!h || m < 0 || n < 0 || (elem_size != 4 && elem_size != 8)) return SPMM_ERR_INVALID_ARGUMENT;
     if (!is_current(h->device)) return SPMM_ERR_INVALID_ARGUMENT;
-    return ensure_scratch(h, layout_for(m, n, elem_size, long_grid_of(h)).total);
+    return ensure_scratch(h, layout_for(m, n, elem_size, long_grid_of(h)).total, nullptr);
 }
 
 spmm_status_t spmm_csr_f32(spmm_handle_t h, float alpha, const int32_t* row_ptr,
@@ -1045,9 +1072,9 @@ spmm_status_t spmm_measure_fp64_fma_rate(spmm_handle_t h, double* fma_per_second
     // to cover the pipe's latency
     const int grid = 4 * h->num_sms;
     const int iters = 2048;
-    spmm_status_t s = ensure_scratch(h, (size_t)grid * 256 * sizeof(double));
+    spmm_status_t s = ensure_scratch(h, (size_t)grid * 256 * sizeof(double), nullptr);
     if (s != SPMM_OK) return s;
-    double* sink = static_cast<double*>(h->scratch);
+    double* sink = static_cast<double*>(h->scratch.at);
     cudaEvent_t e0 = nullptr, e1 = nullptr;
     if (cudaEventCreate(&e0) != cudaSuccess || cudaEventCreate(&e1) != cudaSuccess) {
         cudaGetLastError();

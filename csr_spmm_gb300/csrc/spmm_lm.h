@@ -17,8 +17,8 @@ inline int lm_elem_size(spmm_type_t t) { return t == SPMM_F32 ? 4 : 2; }
 // ---- the handle, for spmm_lm_api.cu (spmm_api.cu) ----
 // The current device must be the handle's; *num_sms is its SM count.
 spmm_status_t lm_device(spmm_handle_t h, int* num_sms);
-// The handle's scratch for these operators, grown to at least `bytes`.
-spmm_status_t lm_scratch(spmm_handle_t h, size_t bytes, char** base);
+// The handle's scratch for these operators, grown to at least `bytes` for a call on `st`.
+spmm_status_t lm_scratch(spmm_handle_t h, size_t bytes, cudaStream_t st, char** base);
 
 // ---- embedding and its gradient (spmm_embed.cu) ----
 struct EmbedParams {

@@ -39,7 +39,7 @@ spmm_status_t spmm_reserve_lm(spmm_handle_t h, int64_t rows, int64_t dim) {
     if (s != SPMM_OK) return s;
     char* base = nullptr;
     return lm_scratch(h, std::max(embed_grad_scratch_upto(rows, dim),
-                                  norm_grad_scratch(rows, dim, sms)), &base);
+                                  norm_grad_scratch(rows, dim, sms)), nullptr, &base);
 }
 
 spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale, const int32_t* ids,
@@ -74,12 +74,12 @@ spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t
     spmm_status_t s = lm_device(h, &sms);
     if (s != SPMM_OK) return s;
     char* scratch = nullptr;
-    s = lm_scratch(h, embed_grad_scratch(tokens, dim), &scratch);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    s = lm_scratch(h, embed_grad_scratch(tokens, dim), st, &scratch);
     if (s != SPMM_OK) return s;
     const EmbedGradParams p{ids,       tokens, dout, ld_dout, dtable,
                             ld_dtable, vocab,  dim,  scale,   beta};
-    return launched(launch_embedding_grad(type, grad_type, p, scratch, sms,
-                                          reinterpret_cast<cudaStream_t>(stream)));
+    return launched(launch_embedding_grad(type, grad_type, p, scratch, sms, st));
 }
 
 spmm_status_t spmm_layer_norm(spmm_handle_t h, spmm_type_t type, spmm_type_t param_type,
@@ -116,13 +116,13 @@ spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_
     spmm_status_t s = lm_device(h, &sms);
     if (s != SPMM_OK) return s;
     char* scratch = nullptr;
-    s = lm_scratch(h, norm_grad_scratch(rows, dim, sms), &scratch);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    s = lm_scratch(h, norm_grad_scratch(rows, dim, sms), st, &scratch);
     if (s != SPMM_OK) return s;
     const NormGradParams p{dy, ld_dy, x,     ldx,     mean,  rstd, weight, rows,
                            dim, dx,   ld_dx, dweight, dbias, reinterpret_cast<float*>(scratch),
                            nullptr};
-    return launched(launch_layer_norm_grad(type, param_type, p, sms,
-                                           reinterpret_cast<cudaStream_t>(stream)));
+    return launched(launch_layer_norm_grad(type, param_type, p, sms, st));
 }
 
 spmm_status_t spmm_token_logprob(spmm_handle_t h, spmm_type_t type, float alpha,

@@ -32,7 +32,11 @@
  * returns.  The handle owns its scratch memory (row bins, long-row partial
  * sums) and grows it on demand; growth calls cudaMalloc/cudaFree, which
  * synchronise the device, so reserve it first (spmm_reserve) when the call
- * will be captured in a CUDA graph.  C must not overlap A or B.
+ * will be captured in a CUDA graph.  A graph holds the scratch that its calls
+ * used: that buffer stays until spmm_destroy, also when a later call grows the
+ * scratch, and a graph may not be replayed after the handle's spmm_destroy (nor
+ * beside other calls on the handle, as for streams below).  C must not overlap
+ * A or B.
  *
  * Asynchrony: the products are enqueued on `stream` (a cudaStream_t passed as
  * void*; NULL means the legacy default stream) and return without
@@ -465,8 +469,10 @@ spmm_status_t spmm_csr_f32_noalloc(float alpha,
  * handle's (SPMM_ERR_INVALID_ARGUMENT).  Scratch, where a call needs some, is
  * the handle's own for these operators, grown with cudaMalloc (which
  * synchronises the device): spmm_reserve_lm beforehand makes later calls
- * free of allocation, as stream capture requires.  One stream at a time per
- * handle, as for the products. */
+ * free of allocation, as stream capture requires.  A captured graph's scratch
+ * stays its own until spmm_destroy.  One stream at a time per handle, as for the
+ * products: two gradients on streams that are not ordered would write one
+ * scratch. */
 typedef enum { SPMM_F32 = 0, SPMM_F16 = 1, SPMM_BF16 = 2 } spmm_type_t;
 
 /* Grow the handle's scratch for gradients (spmm_embedding_grad with up to
