@@ -388,7 +388,7 @@ def load_module(name: str):
     path = os.path.join(PKG, "lib", name + ".so")
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing. Run `python -m csr_spmm_gb300.build` "
-                          "(or __graft_entry__.build()).")
+                          "(or __graft_entry__.build()); it says why where it leaves one out.")
     spec = importlib.util.spec_from_file_location(name, path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

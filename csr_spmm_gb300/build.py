@@ -4,8 +4,10 @@ Each translation unit under ``csrc/`` is compiled by its own nvcc process
 (in parallel), then the objects are linked into one shared library on the shared
 CUDA runtime.  Beside it g++ builds two Python modules for short calls: ``_lm_calls.so``
 calls the language-model entry points, ``_torch_outputs.so`` makes the torch wrappers'
-output tensors.  A rebuild happens only when a source,
-header or flag changed (a content hash is kept beside the library).
+output tensors.  The library needs nvcc alone: a module is left out where Python's headers or
+a CUDA build of torch are missing, and one that fails is reported when the library is in place.
+A rebuild happens only when a source, header or flag changed (a content hash is kept
+beside the library).
 
 Run ``python -m csr_spmm_gb300.build`` or call :func:`build`.
 """
@@ -49,9 +51,16 @@ def _runtime_path(nvcc: str) -> list:
     return ["-Xlinker", "-rpath," + lib] if os.path.isdir(lib) else []
 
 
+def _left_out(name: str, why: str) -> None:
+    sys.stderr.write(f"csr_spmm_gb300.build: _{name} is left out ({why}); the language-model "
+                     "wrappers need it, the library does not\n")
+
+
 def _module(name: str, deps, flags, libs, force: bool) -> None:
     """Build csrc/<name>.cpp, a Python module, with the host compiler."""
     src, out = os.path.join(CSRC, name + ".cpp"), os.path.join(LIB_DIR, "_" + name + ".so")
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return _left_out(name, "no Python.h")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", src, "-I", INCLUDE,
            "-isystem", sysconfig.get_paths()["include"]] + flags + libs
     h = hashlib.sha256(" ".join(cmd).encode())
@@ -79,13 +88,15 @@ def _lm_calls(force: bool = False) -> None:
 
 
 def _torch_outputs(force: bool = False) -> None:
-    """The module that makes the torch wrappers' outputs (none without torch)."""
+    """The module that makes the torch wrappers' outputs (none without torch for CUDA)."""
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return
     torch = list(spec.submodule_search_locations)[0]
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     libs = os.path.join(torch, "lib")
+    if not os.path.exists(os.path.join(libs, "libtorch_cuda.so")):
+        return _left_out("torch_outputs", "torch is built without CUDA")
     _module("torch_outputs", [os.path.join(torch, "version.py")],
             ["-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include")],
             ["-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
@@ -158,8 +169,6 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), out: str =
     with ThreadPoolExecutor(max_workers=max(1, min(len(units), os.cpu_count() or 4))) as ex:
         modules = [ex.submit(m, force) for m in (_torch_outputs, _lm_calls) if out == LIB]
         objs = list(ex.map(compile_one, units))
-        for m in modules:
-            m.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + LINK_FLAGS + _runtime_path(nvcc) + ["-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -168,6 +177,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), out: str =
     os.replace(tmp, out)
     with open(stamp, "w") as f:
         f.write(digest + "\n")
+    for m in modules:                        # a failure of theirs, now that the library is there
+        m.result()
     return out
 
 
