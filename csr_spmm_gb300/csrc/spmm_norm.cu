@@ -164,9 +164,11 @@ enum class Fit { ALL, WHOLE, EDGES };
 
 // A row in registers, K accesses of W elements per lane: read once, one exchange
 // between its warps.  The bound is HBM (read x, write y) as long as an element costs
-// few instructions: 65,521 f16 rows of 8192 took 476 us at 27 per element and take 366 at 18,
-// two elements at a time and without a branch (5.9 TB/s, 86% of the copy rate; 40,000
-// binary32 rows of 2048: 101 us, 95%).  Rows with edges walk the matrix with a
+// few instructions: 65,521 f16 rows of 8192 took 476 us at 27 per element and take 368 at 16,
+// two elements at a time and, but for the second look, without a branch (5.8 TB/s, 86% of the
+// copy rate; 40,000 binary32 rows of 2048: 101 us, 95%; 60,000 x 2001 bf16 111 us, 64%).  A
+// second look at one of the eight warps' parts of every row (an outlier at its first element)
+// makes that 424 us.  Rows with edges walk the matrix with a
 // fixed grid and keep the parameters in shared memory in binary32, (weight, bias)
 // of column c at [c mod W][c / W]: wherever a row starts, a warp reads neighbours.
 // The others have a block of threads each and read the parameters from L1.  (Measured and
@@ -329,6 +331,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
             row_barrier(in_block, threads);
             if (l.warps >= 8) {
                 // a lane for each warp's part: 10 shuffles instead of 7 instructions for each
+                // (18,000 x 16,384 bf16, 16 warps: 230 us, 254 with the loop below)
                 const float4 v = lane < l.warps ? s[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 off = warp_sum(v.x) * per_dim;
                 squares = warp_sum(fmaf(v.w * (v.y - off), v.y - off, v.z));

@@ -8,6 +8,14 @@ or bfloat16; ids, targets and indices are int32.  Each call is enqueued on
 ``stream`` (default: torch's current stream) and returns without waiting; new
 outputs are allocated for that stream, and the inputs' memory is held until
 the stream has used it.
+
+One stream at a time per handle: :func:`embedding_grad` and :func:`layer_norm_grad` use the
+handle's scratch, which their calls on two streams would share without an order.  Use a handle
+for each stream, or order the streams.  The other functions use no scratch.
+
+Nothing is recorded for autograd: results are detached also where an argument requires a
+gradient, and the gradients are functions of their own.  New outputs come straight from
+torch's caching allocator, so modes that intercept torch.empty do not see them.
 """
 from __future__ import annotations
 
@@ -136,7 +144,8 @@ def embedding_grad(handle, ids, dout, dtable, scale: float = 1.0, beta: float = 
 
     ``dout`` is [tokens, dim]; ``dtable`` is [vocabulary, dim] in dout's dtype
     or float32.  beta = 0 writes every row; beta = 1 adds to the rows of the
-    ids that occur and leaves the others alone.
+    ids that occur and leaves the others alone.  Uses the handle's scratch: one stream at a
+    time.
     """
     code, grad_code = _type(dout, "dout"), _type(dtable, "dtable")
     if grad_code != code and grad_code != _lib.SPMM_F32:
@@ -200,7 +209,8 @@ def layer_norm_grad(handle, dy, x, mean, rstd, weight=None, bias: bool = True, o
 
     ``mean`` and ``rstd`` are what the forward pass returned.  dweight is None
     without a weight, dbias with ``bias=False``; both have the weight's dtype
-    (dbias x's dtype without a weight).  ``out`` receives dx; it may be ``dy``.
+    (dbias x's dtype without a weight).  ``out`` receives dx; it may be ``dy``.  Uses the
+    handle's scratch: one stream at a time.
     """
     code = _type(x, "x")
     rows, dim, ld = _matrix(x, "x")

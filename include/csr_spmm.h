@@ -500,8 +500,11 @@ spmm_status_t spmm_embedding(spmm_handle_t h, spmm_type_t type, float scale,
  * sorted by id on the device (stable), and each row's sum is taken in binary32
  * over pieces of consecutive sorted tokens whose bounds depend on `tokens`
  * and `dim` alone, then over the pieces in order.  Scratch: two 8-byte keys per
- * token, and at most 8 bytes per element of dout (for long inputs about 9 MB
- * or 1/16 byte per element, the larger).  tokens <= 2^30. */
+ * token, and for each piece two binary32 rows of dim columns (rounded up to a
+ * multiple of 8, plus 8) and 12 bytes for each 256 columns or part of them, and
+ * 12 more.  There is at most one piece per token, and no more than 4097 divided by
+ * those 256s, or tokens / 128, the larger, plus one: for long inputs about 9 MB
+ * or 1/16 byte per element of dout.  tokens <= 2^30. */
 spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t grad_type,
                                   float scale, const int32_t *ids, int64_t tokens,
                                   const void *dout, int64_t ld_dout, float beta,
@@ -513,8 +516,10 @@ spmm_status_t spmm_embedding_grad(spmm_handle_t h, spmm_type_t type, spmm_type_t
  * 1 / sqrt(mean of the squared deviations + eps).  weight and bias (dim
  * entries, either may be NULL: 1 and 0) have type `param_type`, which is
  * `type` or SPMM_F32; mean and rstd are binary32 outputs for the gradient and
- * may be NULL.  The deviations are taken from the row's own mean in a second
- * pass over the row, so a row far from zero loses nothing.  y may be x.
+ * may be NULL.  The sums are of differences to elements of the row, and the
+ * deviations are taken from its own mean, so a row far from zero loses nothing:
+ * the mean is off by its own rounding, and a constant row's is the constant.  y may
+ * be x.
  * eps >= 0 (a constant row with eps == 0 gives NaN, as the formula does).
  * rows == 0 or dim == 0: nothing is done.  One launch, no scratch. */
 spmm_status_t spmm_layer_norm(spmm_handle_t h, spmm_type_t type, spmm_type_t param_type,
