@@ -246,20 +246,24 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < Vec<T, W>::WORDS; ++i) held[k].w[i] = in(k) ? held[k].w[i] : 0;
-        // b and q, 0 where they are infinite or NaN
+        // b and q, 0 where they are infinite or NaN.  q is the middle one of three, so that a few
+        // columns of large values do not put it far from the mean, whose rounding would be that
+        // of the distance; b too in rows with edges, where a second look costs more (with a
+        // first column far from the others 60,000 x 2001 bf16 would take 181 us), but not in the
+        // others, whose lanes would have to ask twice more (65,521 x 8192 f16 377 us).
         auto finite = [](float v) { return fabsf(v) < INFINITY ? v : 0.0f; };
+        auto middle = [&](const T* of) {
+            const float u = to_f32(of[0]), v = to_f32(of[dim / 2]), w = to_f32(of[dim - 1]);
+            return finite(fmaxf(fminf(u, v), fminf(fmaxf(u, v), w)));
+        };
         float base, pivot;
         if constexpr (EDGES) {
-            // the one between the others of three, since a second look costs rows with edges
-            // more: with a first column far from the others 60,000 x 2001 bf16 would take 181 us
-            const T* from = live ? row : x.base;
-            const float a = to_f32(from[0]), b = to_f32(from[dim / 2]), c = to_f32(from[dim - 1]);
-            base = pivot = finite(fmaxf(fminf(a, b), fminf(fmaxf(a, b), c)));
+            base = pivot = middle(live ? row : x.base);
         } else {
             float f[W];
             unpack(held[0], f);
             base = pivot = finite(__shfl_sync(ALL, f[0], lane & ~(l.lanes - 1)));
-            if (l.warps > 1) pivot = finite(to_f32(row[0]));
+            if (l.warps > 1) pivot = middle(row);
         }
         uint64_t d1 = pair(0.0f, 0.0f), d2 = d1;
 #pragma unroll
@@ -315,6 +319,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
             lanes_sum(again, squares_again, l.lanes);
             if (far) {
                 base = better;
+                if (l.warps == 1) pivot = better;
                 deviations = again;
                 squares = squares_again;
             }

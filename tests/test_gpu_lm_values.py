@@ -150,3 +150,19 @@ def test_layer_norm_of_rows_that_hardly_vary(cs, handle, dim, rows):  # noqa: F8
     _near(_np(rstd), r[:, 0], d_rstd[:, 0], "rstd")
     _near(_np(y), dev * r, d_mean * (r + d_rstd) + np.abs(dev) * d_rstd + 4 * ref.U * np.abs(dev * r),
           "y")
+
+
+@pytest.mark.parametrize("rows", [5, 400])
+@pytest.mark.parametrize("dim", [64, 444, 600, 2276, 2277, 5312, 8200])
+@pytest.mark.parametrize("t", TYPES)
+def test_layer_norm_of_rows_with_outliers(cs, handle, t, dim, rows):  # noqa: F811
+    """Columns of large values, where rows and parts of rows begin among them: neither the mean
+    nor the deviations lose digits to them."""
+    rng = np.random.default_rng(dim + rows)
+    for columns in (slice(0, 1), slice(None, None, 512), slice(None, None, dim // 3 + 1)):
+        x = torch.from_numpy(rng.standard_normal((rows, dim)) * 1.5 + 0.25).to(DT[t])
+        x[:, columns] *= 60
+        y, mean, rstd = cs.layer_norm(handle, x.cuda(), eps=1e-3)
+        want = ref.layer_norm(x.double().numpy(), 1.0, 0.0, float(np.float32(1e-3)), t)
+        for g, (v, bound), what in zip((y, mean, rstd), want, ("y", "mean", "rstd")):
+            _near(_np(g), v, bound, what)
