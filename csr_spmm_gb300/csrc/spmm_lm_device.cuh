@@ -244,7 +244,9 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // Two binary32 operations in one instruction (sm_100 and later); each half is
-// rounded as the single operation would be.
+// rounded as the single operation would be, but for a mul2 whose product an add2 takes:
+// the two become one fma2 (measured), where a product has to be rounded first use
+// __fmul_rn.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));

@@ -174,11 +174,16 @@ __device__ __forceinline__ Sums join(Sums a, float c, float low) {
     return {m, warp_sum(a.s), warp_sum(a.u)};
 }
 
-// Log probability of a logit, alpha x - lse in one rounding.  alpha x counts in binary32: a
-// logit that alpha takes below its range is masked, whatever lse would make of it.
+// From here on a logit's and lse's last places (1/8) count beside the logarithms that tell them
+// apart.  z = alpha x is a binary32 number there, like lse: the places that it has lost would
+// otherwise show in z - lse (equal logits of 1e37 would differ from their lse by 1e29).  Below,
+// alpha x joins a sum in one rounding, which is closer to the exact one.
+constexpr float LARGE = 1048576.0f;
+// Log probability of a logit.  One that alpha takes below binary32's range is masked, whatever
+// lse would make of it.
 __device__ __forceinline__ float log_p(float alpha, float x, float lse) {
     const float z = __fmul_rn(alpha, x);
-    return z == -INFINITY ? z - lse : fmaf(alpha, x, -lse);
+    return fabsf(z) < LARGE ? fmaf(alpha, x, -lse) : z - lse;
 }
 
 struct RowShared {
@@ -596,9 +601,11 @@ __global__ __launch_bounds__(32 * LP_WARPS, 4) void logprob_rows(LogprobParams p
     const bool nan = !none && !(fabsf(z) < INFINITY);
     const float log_s = log2f(a.s);
     const float left = far ? 0.0f : fmaf(-a.m, c, base_of(a.m, c, low));
-    const float lse = none  ? -INFINITY
-                      : nan ? NAN
-                            : fmaf(p.alpha, a.m, LN2 * (log_s + left));
+    const float above = LN2 * (log_s + left);
+    const float lse = none               ? -INFINITY
+                      : nan              ? NAN
+                      : fabsf(z) < LARGE ? fmaf(p.alpha, a.m, above)
+                                         : z + above;
     if (tid == 0) {
         if (p.lse) p.lse[r] = lse;
         if (p.entropy) p.entropy[r] = none ? 0.0f : nan ? NAN : LN2 * (log_s - a.u / a.s);
@@ -653,8 +660,22 @@ cudaError_t launch_forward(const LogprobParams& p, int num_sms, cudaStream_t st)
 constexpr int LG_THREADS = 256;
 constexpr int LG_BATCH = 4;          // accesses in flight per thread
 
+// The columns c, c + stride, ... of a row whose lse is LARGE.  Seldom, and not inlined: a second
+// form of the loop below would take its registers (8192 x 131,072 bf16 712 us, 683 with a
+// choice at each element).
+template <typename T>
+__device__ __noinline__ void grad_one_by_one(const T* x, T* dx, int64_t vocab, int64_t c,
+                                             int64_t stride, float alpha, float lse, float de,
+                                             float k, int target, float up) {
+    for (; c < vocab; c += stride) {
+        const float q = max_nan(__fmul_rn(alpha, to_f32(x[c])) - lse, -200.0f);
+        const float d = exp2_approx(q * LOG2E) * fmaf(-de, q, k);
+        dx[c] = from_f32<T>(c == target ? d + up : d);
+    }
+}
+
 // dx = p * (-(up + de * entropy) - de * q) (+ up at the target), with alpha in up
-// and de, q = alpha x - lse and p = exp(q).  A row takes `pieces` consecutive
+// and de, q = z - lse (z = alpha x, a binary32 number where lse is LARGE) and p = exp(q).  A row takes `pieces` consecutive
 // blocks, so that blocks in flight together work on neighbouring memory; W == 1
 // where logits and dlogits lie differently against 16-byte boundaries.  The
 // bound is HBM (read x, write dx): 8192 rows of 131,072 bf16 645 us, 6.7 TB/s (98% of
@@ -679,6 +700,11 @@ __global__ __launch_bounds__(LG_THREADS) void logprob_grad_rows(LogprobGradParam
     const float k = p.dentropy ? -fmaf(de, p.entropy[r], up) : -up;
     const int64_t at_target = has ? (int64_t)target + off : -1;
     const bool empty = lse == -INFINITY;
+    if (fabsf(lse) >= LARGE && !empty) {
+        grad_one_by_one(x, dx + off, p.vocab, (int64_t)piece * step + threadIdx.x,
+                        (int64_t)pieces * step, p.alpha, lse, de, k, has ? target : -1, up);
+        return;
+    }
     for (int64_t j0 = (int64_t)piece * step * LG_BATCH + threadIdx.x; j0 < nvec;
          j0 += (int64_t)pieces * step * LG_BATCH) {
         Vec<T, W> v[LG_BATCH];       // packed until all are on their way

@@ -558,8 +558,9 @@ spmm_status_t spmm_layer_norm_grad(spmm_handle_t h, spmm_type_t type, spmm_type_
  * +inf among the logits makes the row's lse, entropy, logprob and top_logprob
  * NaN; NaNs are never alternatives.  z is formed in binary32, so a finite logit
  * that alpha takes beyond its range counts as an infinite one (below: masked;
- * above: the row is NaN).  The order of the alternatives is that of the logits
- * themselves, before alpha.
+ * above: the row is NaN), and where lse is 2^20 or more in magnitude z - lse is the
+ * difference of two binary32 numbers (below, it is rounded once).  The order of the
+ * alternatives is that of the logits themselves, before alpha.
  * All outputs but top_index are binary32.  targets and logprob may be NULL
  * together, entropy and lse each, top_logprob and top_index when top_k == 0.
  * 0 <= top_k <= 32.  One pass over the logits, one launch, no scratch. */

@@ -166,3 +166,47 @@ def test_layer_norm_of_rows_with_outliers(cs, handle, t, dim, rows):  # noqa: F8
         want = ref.layer_norm(x.double().numpy(), 1.0, 0.0, float(np.float32(1e-3)), t)
         for g, (v, bound), what in zip((y, mean, rstd), want, ("y", "mean", "rstd")):
             _near(_np(g), v, bound, what)
+
+
+@pytest.mark.parametrize("rows", [7, 700])
+@pytest.mark.parametrize("vocab", [100, 5003])
+@pytest.mark.parametrize("t,alpha", [("f32", 0.7), ("f32", 1.25), ("f32", 0.3), ("bf16", 0.7),
+                                     ("bf16", 1.1), ("f16", 0.7), ("f16", 900.7)])
+def test_logits_whose_last_place_is_larger_than_their_differences(cs, handle, t, alpha, vocab,  # noqa: F811
+                                                                  rows):
+    """Rows of equal logits of large magnitude (a type's lowest values as masks throughout): z and
+    lse are binary32 numbers some of whose places are lost, but lost alike: no log probability
+    is above 0 or below by more than a place, and the gradient is the formula's of those numbers."""
+    low, high = float(torch.finfo(DT[t]).min), float(torch.finfo(DT[t]).max)
+    values = torch.tensor([low / 4, high / 8, low / 3, -6.1e4, 5.3e4, low / 1000, 777.0],
+                          device="cuda").to(DT[t])
+    x = values.repeat(rows // 7)[:, None].expand(rows, vocab).contiguous()
+    x[:, 3] = -INF
+    targets = torch.full((rows,), vocab - 1, dtype=torch.int32, device="cuda")
+    lp, ent, lse, best, index = cs.token_logprob(handle, x, targets, alpha=alpha, top=2)
+    z = np.float32(alpha) * _np(x[:, -1]).astype(np.float32)
+    assert z.dtype == np.float32 and np.isfinite(z).all()
+    place = np.spacing(np.abs(z)).astype(np.float64)
+    n = vocab - 1
+    # lse and z are rounded once each, log(n) beside them; their difference once more
+    bound = 1.01 * place + ref.U * (ref.chain(vocab) + 16) * (1 + np.log(n))
+    _near(_np(lse), z.astype(np.float64) + np.log(n), bound, "lse")
+    _near(_np(lp), np.full(rows, -np.log(n)), bound + place / 2, "logprob")
+    assert bool((lp <= 0).all()) and torch.equal(best, lp[:, None].expand(rows, 2))
+    assert index.tolist() == [[0, 1]] * rows
+    _near(_np(ent), np.full(rows, np.log(n)), ref.U * (ref.chain(vocab) + 24) * np.log(n), "entropy")
+    up = torch.full((rows,), -1.0, device="cuda")
+    got = cs.token_logprob_grad(handle, x, targets, lse, ent, up, 0.5 * up, alpha=alpha)
+    a32 = float(np.float32(alpha))
+    # below 2^20, z - lse is taken in one rounding
+    exact = a32 * _np(x[:, -1])
+    q = np.where(np.abs(_np(lse)) < 2.0 ** 20, exact, z.astype(np.float64)) - _np(lse)
+    p = np.exp(q)
+    want = np.zeros((rows, vocab))
+    want += (a32 * p * (1 + 0.5 * (q + _np(ent))))[:, None]
+    want[:, -1] -= a32
+    want[:, 3] = 0.0
+    # the exponential is off by 8 U and its argument by 2 U of itself; the terms by their roundings
+    scale = a32 * (p * (1 + np.abs(q) + np.abs(_np(ent))) + 1)[:, None]
+    _near(_np(got), want, 40 * ref.U * (1 + np.abs(q))[:, None] * scale + ref.rounding(t, want),
+          "dlogits")
