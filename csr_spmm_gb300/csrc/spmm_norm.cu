@@ -164,11 +164,11 @@ enum class Fit { ALL, WHOLE, EDGES };
 
 // A row in registers, K accesses of W elements per lane: read once, one exchange
 // between its warps.  The bound is HBM (read x, write y) as long as an element costs
-// few instructions: 65,521 f16 rows of 8192 took 476 us at 27 per element and take 368 at 16,
-// two elements at a time and, but for the second look, without a branch (5.8 TB/s, 86% of the
-// copy rate; 40,000 binary32 rows of 2048: 101 us, 95%; 60,000 x 2001 bf16 111 us, 64%).  A
+// few instructions: 65,521 f16 rows of 8192 took 476 us at 27 per element and take 363 at 17,
+// two elements at a time and, but for the second look, without a branch (5.9 TB/s, 87% of the
+// copy rate; 40,000 binary32 rows of 2048: 101 us, 95%; 60,000 x 2001 bf16 110 us, 64%).  A
 // second look at one of the eight warps' parts of every row (an outlier at its first element)
-// makes that 424 us.  Rows with edges walk the matrix with a
+// makes 424 us of 367 (calls back to back).  Rows with edges walk the matrix with a
 // fixed grid and keep the parameters in shared memory in binary32, (weight, bias)
 // of column c at [c mod W][c / W]: wherever a row starts, a warp reads neighbours.
 // The others have a block of threads each and read the parameters from L1.  (Measured and
