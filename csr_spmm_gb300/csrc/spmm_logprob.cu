@@ -675,10 +675,10 @@ __device__ __noinline__ void grad_one_by_one(const T* x, T* dx, int64_t vocab, i
 }
 
 // dx = p * (-(up + de * entropy) - de * q) (+ up at the target), with alpha in up
-// and de, q = z - lse (z = alpha x, a binary32 number where lse is LARGE) and p = exp(q).  A row takes `pieces` consecutive
-// blocks, so that blocks in flight together work on neighbouring memory; W == 1
-// where logits and dlogits lie differently against 16-byte boundaries.  The
-// bound is HBM (read x, write dx): 8192 rows of 131,072 bf16 645 us, 6.7 TB/s (98% of
+// and de, q = z - lse (z = alpha x, a binary32 number where lse is LARGE) and
+// p = exp(q).  A row takes `pieces` consecutive blocks, so that blocks in flight
+// together work on neighbouring memory; W == 1 where logits and dlogits lie
+// differently against 16-byte boundaries.  The bound is HBM (read x, write dx): 8192 rows of 131,072 bf16 645 us, 6.7 TB/s (98% of
 // the copy rate; 986 us when each access was unpacked before the next was sent).
 template <typename T, int W>
 __global__ __launch_bounds__(LG_THREADS) void logprob_grad_rows(LogprobGradParams p, int pieces) {

@@ -292,11 +292,12 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
         halves(d2, lo, hi);
         squares = lo + hi;
         lanes_sum(deviations, squares, l.lanes);
-        const bool far = deviations * deviations * per_count > 0.94f * squares;
+        float off = deviations * per_count;
+        const bool far = deviations * off > 0.94f * squares;
         if (__any_sync(ALL, far)) {
             // From memory again (y, which may be x, is written behind the exchange below, or by
             // these lanes): a second use of `held` here would cost every row registers.
-            const float better = fmaf(deviations, per_count, base);
+            const float better = base + off;
             float again = 0.0f, squares_again = 0.0f;
 #pragma unroll 1
             for (int k = 0; k < K; ++k) {
@@ -321,12 +322,13 @@ __global__ __launch_bounds__(1024) void norm_rows(NormParams p, Layout l, int64_
                 base = better;
                 if (l.warps == 1) pivot = better;
                 deviations = again;
+                off = again * per_count;
                 squares = squares_again;
             }
         }
-        float off = deviations * per_count;
-        squares = fmaf(-deviations, off, squares);
-        squares = squares < 0.0f ? 0.0f : squares;   // NaN stays
+        // what is left is at least 6% of them; squares beyond binary32 stay so (rstd 0), unless there
+        // is an infinite element (NaN)
+        squares = fmaf(squares < INFINITY ? -deviations : 0.0f, off, squares);
         off += base - pivot;
         if (l.warps > 1) {
             // two sets of slots in turn: one barrier per row keeps them apart

@@ -210,3 +210,22 @@ def test_logits_whose_last_place_is_larger_than_their_differences(cs, handle, t,
     scale = a32 * (p * (1 + np.abs(q) + np.abs(_np(ent))) + 1)[:, None]
     _near(_np(got), want, 40 * ref.U * (1 + np.abs(q))[:, None] * scale + ref.rounding(t, want),
           "dlogits")
+
+
+@pytest.mark.parametrize("rows", [3, 350])
+@pytest.mark.parametrize("dim", [5, 64, 1001, 4096, 20001])
+def test_layer_norm_beyond_the_range_of_squares(cs, handle, dim, rows):  # noqa: F811
+    """Deviations whose squares overflow have rstd 0, so y is the bias; an infinite element makes
+    the row NaN."""
+    x = torch.randn(rows, dim, device="cuda") * 1e25
+    x[:, 0] = 3e25
+    w = torch.linspace(0.5, 2.0, dim, device="cuda")
+    b = torch.linspace(-1.0, 1.0, dim, device="cuda")
+    y, mean, rstd = cs.layer_norm(handle, x, w, b)
+    assert not bool(rstd.any()) and torch.equal(y, b.expand(rows, dim))
+    assert bool(((mean.double() - x.double().mean(1)).abs() < 1e21).all())
+    x[1, dim // 2] = INF
+    x[2, dim - 1] = -INF
+    y, mean, rstd = cs.layer_norm(handle, x, w, b)
+    assert bool(y[1:3].isnan().all()) and bool(rstd[1:3].isnan().all())
+    assert torch.equal(y[0], b)
